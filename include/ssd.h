@@ -315,6 +315,146 @@ SSD_API ssd_status_t ssd_gated_rmsnorm(const ssd_shape_t* shape, const void* y, 
                                        const float* weight, int64_t group_size, float eps,
                                        void* out, void* stream);
 
+/* ---- The short causal convolution before the layer. ----
+ * Knowl 6, step 2 of the Mamba-2 block: x, B and C pass through a depthwise
+ * convolution of W taps along the sequence, each channel on its own, before
+ * they enter the layer:
+ *     v[t,c] = bias[c] + sum_{k<W} weight[c,k] * u[t - (W-1) + k, c]
+ *     y[t,c] = v[t,c] / (1 + exp(-v[t,c]))        (silu = 1; silu = 0: y = v)
+ * where u before the first token is the sequence's initial state (its last
+ * W - 1 tokens, oldest first), or 0. The output is split by channel into up to
+ * three contiguous tensors, as ssd_fwd takes x, B and C.
+ */
+
+/* Distances in elements between the batch rows and between the tokens of an
+ * input whose channels are contiguous: an input can be a slice of a wider
+ * projection's rows. Both >= 0 (0 repeats a row). */
+typedef struct {
+    int64_t batch;
+    int64_t row;
+} ssd_strides_t;
+
+typedef struct {
+    int64_t batch;            /* b >= 0                                              */
+    int64_t seqlen;           /* T >= 0                                              */
+    int64_t channels;         /* C >= 1                                              */
+    int64_t width;            /* W in {2, 3, 4} taps                                 */
+    int64_t out_channels[3];  /* channels of y0, y1, y2: their sum is C, each >= 0   */
+    ssd_strides_t u;          /* strides of u                                        */
+    int32_t dtype;            /* ssd_dtype_t of u, y0, y1, y2 and the states         */
+    int32_t silu;             /* 1: SiLU after the convolution; 0: none              */
+} ssd_conv_shape_t;
+
+/*
+ * Whole prompts.
+ *   u                  [b, T, C] dtype, strides as given.
+ *   weight             [C, W] fp32; tap W - 1 takes the current token.
+ *   bias               [C] fp32 or NULL (0).
+ *   initial_states     [b, W-1, C] dtype or NULL (zeros).
+ *   y0, y1, y2         [b, T, out_channels[i]] dtype, contiguous; NULL where
+ *                      out_channels[i] is 0.
+ *   final_states       [b, W-1, C] dtype or NULL (not written): the last W - 1
+ *                      tokens of (initial_states | u), so of both when T < W - 1.
+ * fp32 arithmetic, y rounded once to dtype. Pointers are aligned to their
+ * element; 16-byte aligned tensors, strides and splits are read and written 16
+ * bytes at a time. No output may overlap u's span (first to last element), any
+ * other input or another output. One kernel launch, no workspace.
+ */
+SSD_API ssd_status_t ssd_causal_conv1d(const ssd_conv_shape_t* shape, const void* u, const float* weight,
+                                       const float* bias, const void* initial_states,
+                                       void* y0, void* y1, void* y2, void* final_states, void* stream);
+
+/*
+ * Packed documents (as ssd_fwd_varlen: batch = 1, document k is tokens
+ * cu_seqlens[k] .. cu_seqlens[k+1] - 1 of the pack), each its own sequence.
+ *   cu_seqlens         DEVICE int32 [n_docs + 1], from 0, non-decreasing, at most
+ *                      T. Rows behind the last document are left as they were.
+ *                      It is read on the device: the offsets of a malformed list
+ *                      are clamped into [0, T], so that nothing outside the
+ *                      tensors is read or written; y and the states are then
+ *                      unspecified.
+ *   n_docs             >= 0 (0 only with T = 0: nothing to do), at most 2^24.
+ *   initial_states, final_states   [n_docs, W-1, C] dtype or NULL; an empty
+ *                      document's final state is its initial state.
+ */
+SSD_API ssd_status_t ssd_causal_conv1d_varlen(const ssd_conv_shape_t* shape, const void* u,
+                                              const float* weight, const float* bias,
+                                              const int32_t* cu_seqlens, int64_t n_docs,
+                                              const void* initial_states,
+                                              void* y0, void* y1, void* y2, void* final_states,
+                                              void* stream);
+
+/*
+ * Decoding: shape->seqlen tokens per batch row (usually 1) from `state`
+ * [b, W-1, C] dtype, which is overwritten in place with the last W - 1 tokens.
+ * state must not overlap any input or output. One kernel launch.
+ */
+SSD_API ssd_status_t ssd_causal_conv1d_step(const ssd_conv_shape_t* shape, const void* u,
+                                            const float* weight, const float* bias, void* state,
+                                            void* y0, void* y1, void* y2, void* stream);
+
+/* ---- The selective scan with a diagonal A. ----
+ * The general diagonal form of the recurrence (Knowl 3; ssd_fwd's is the scalar
+ * times identity): every channel d of D has its own step size dt[t,d] and its
+ * own N decay rates A[d,:], and a state of N numbers. Per batch row:
+ *     dt'[t,d]  = softplus(dt[t,d] + dt_bias[d])     (dt_softplus = 1)
+ *               = dt[t,d] + dt_bias[d]               (dt_softplus = 0)
+ *     h_t[d,n]  = exp(dt'[t,d] * A[d,n]) * h_{t-1}[d,n] + dt'[t,d] * u[t,d] * B[t,g,n]
+ *     y[t,d]    = sum_n C[t,g,n] * h_t[d,n] + D[d] * u[t,d]
+ *     y[t,d]   *= z[t,d] / (1 + exp(-z[t,d]))        (z given)
+ * with g = d / (channels / ngroups), softplus(v) = log(1 + exp(v)).
+ */
+typedef struct {
+    int64_t batch;        /* b >= 0                                          */
+    int64_t seqlen;       /* T >= 0                                          */
+    int64_t channels;     /* D >= 1                                          */
+    int64_t ngroups;      /* G >= 1, divides D                               */
+    int64_t dstate;       /* N in [1, 256]                                   */
+    ssd_strides_t u, dt, z, B, C;   /* strides of the inputs (z's unused without z) */
+    int32_t dtype;        /* ssd_dtype_t of u, z, B, C and y                 */
+    int32_t dt_dtype;     /* ssd_dtype_t of dt: SSD_F32 or dtype             */
+    int32_t dt_softplus;  /* 0 or 1                                          */
+    int32_t reserved;     /* must be 0                                       */
+} ssd_selective_shape_t;
+
+/*
+ * Whole prompts.
+ *   u, dt, z           [b, T, D], strides as given; z NULL: no gate.
+ *   A                  [D, N] fp32 (not checked for sign; a decay above 1 that
+ *                      overflows fp32 gives inf or NaN).
+ *   B, C               [b, T, G, N], strides as given ([G, N] contiguous).
+ *   D, dt_bias         [D] fp32 or NULL (0).
+ *   initial_states     [b, D, N] fp32 or NULL (zeros).
+ *   y                  [b, T, D] dtype, contiguous.
+ *   final_states       [b, D, N] fp32 or NULL (not written).
+ * States, decays and sums are fp32 for both dtypes, y is rounded once. Pointers
+ * are aligned to their element. No output may overlap an input's span or another
+ * output. One kernel launch, no workspace, no order of arithmetic that changes
+ * from call to call.
+ */
+SSD_API ssd_status_t ssd_selective_scan(const ssd_selective_shape_t* shape, const void* u, const void* dt,
+                                        const float* A, const void* B, const void* C, const float* D,
+                                        const void* z, const float* dt_bias,
+                                        const float* initial_states, void* y, float* final_states,
+                                        void* stream);
+
+/* Packed documents: batch = 1, cu_seqlens and n_docs as for
+ * ssd_causal_conv1d_varlen, initial_states and final_states [n_docs, D, N]. */
+SSD_API ssd_status_t ssd_selective_scan_varlen(const ssd_selective_shape_t* shape, const void* u,
+                                               const void* dt, const float* A, const void* B,
+                                               const void* C, const float* D, const void* z,
+                                               const float* dt_bias, const int32_t* cu_seqlens,
+                                               int64_t n_docs, const float* initial_states, void* y,
+                                               float* final_states, void* stream);
+
+/* Decoding: shape->seqlen tokens per batch row (usually 1) from `state` [b, D, N]
+ * fp32, read once and overwritten in place (as ssd_step). state must not overlap
+ * any input or y. One kernel launch. */
+SSD_API ssd_status_t ssd_selective_step(const ssd_selective_shape_t* shape, const void* u, const void* dt,
+                                        const float* A, const void* B, const void* C, const float* D,
+                                        const void* z, const float* dt_bias, float* state, void* y,
+                                        void* stream);
+
 /* ---- Sequence (context) parallelism (Knowl 8: the sequence is split along its
  * length across workers; each runs its slice and only the boundary state
  * travels). ----

@@ -25,6 +25,9 @@ Functions
                   segment-aware decays, step by step (the kernels' blueprint).
   chunked()       the block-decomposition algorithm, step by step, fp64.
   gated_rmsnorm() the gate and RMSNorm after the layer (Knowl 6), fp64.
+  causal_conv1d() the short causal convolution before the layer (Knowl 6), fp64.
+  selective_scan() the recurrence with a diagonal A per channel (Knowl 3's general
+                  form restricted to a diagonal), fp64.
 Every function is pinned by ``tests/test_oracle.py`` against closed forms,
 library routines and the identities the pages state.
 """
@@ -413,6 +416,57 @@ def chunked_varlen(x, dt, A, B, C, D=None, cu_seqlens=None, chunk_size=64, initi
         if D is not None:
             y[0, :, h] += D[h] * x[0, :, h]
     return y, final
+
+
+def causal_conv1d(u, weight, bias=None, silu=True, initial_states=None):
+    """Short causal depthwise convolution before the layer (Knowl 6), fp64.
+
+    u [b, T, C], weight [C, W] (the last tap on the current token), bias [C];
+    initial_states [b, W-1, C]: the tokens before the first, or zeros. Returns
+    (y [b, T, C], final_states [b, W-1, C]: the last W - 1 tokens of both).
+    """
+    u, w, bias, init = map(_f64, (u, weight, bias, initial_states))
+    b, T, C = u.shape
+    W = w.shape[1]
+    seq = np.concatenate([np.zeros((b, W - 1, C)) if init is None else init, u], axis=1)
+    v = np.zeros((b, T, C)) if bias is None else np.broadcast_to(bias, (b, T, C)).copy()
+    for t in range(T):
+        for k in range(W):
+            v[:, t] += w[:, k] * seq[:, t + k]
+    return (v / (1.0 + np.exp(-v)) if silu else v), seq[:, T:].copy()
+
+
+def selective_steps(dt, dt_bias=None, dt_softplus=False):
+    """dt + dt_bias, through softplus(v) = log(1 + exp(v)) when asked, fp64."""
+    dt, bias = _f64(dt), _f64(dt_bias)
+    v = dt if bias is None else dt + bias
+    return np.logaddexp(0.0, v) if dt_softplus else v
+
+
+def selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus=False,
+                   initial_states=None):
+    """The recurrence with a diagonal A, token by token, fp64.
+
+    h_t[d,n] = exp(dt_t[d] A[d,n]) h_{t-1}[d,n] + dt_t[d] u_t[d] B_t[g,n],
+    y_t[d] = (sum_n C_t[g,n] h_t[d,n] + D[d] u_t[d]) * SiLU(z_t[d]), g = d // (D / G).
+    u, dt, z [b, T, D], A [D, N], B, C [b, T, G, N], states [b, D, N].
+    """
+    u, A, B, C, D, z, init = map(_f64, (u, A, B, C, D, z, initial_states))
+    dt = selective_steps(dt, dt_bias, dt_softplus)
+    b, T, Dc = u.shape
+    G, N = B.shape[2], B.shape[3]
+    group = np.arange(Dc) // (Dc // G)
+    h = np.zeros((b, Dc, N)) if init is None else init.copy()
+    y = np.zeros((b, T, Dc))
+    for t in range(T):
+        x = (dt[:, t] * u[:, t])[..., None]
+        h = np.exp(dt[:, t, :, None] * A) * h + x * B[:, t, group]
+        y[:, t] = np.sum(C[:, t, group] * h, axis=-1)
+    if D is not None:
+        y = y + D * u
+    if z is not None:
+        y = y * (z / (1.0 + np.exp(-z)))
+    return y, h
 
 
 def rel_err(a, ref) -> float:

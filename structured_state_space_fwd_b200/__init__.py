@@ -21,11 +21,15 @@ import torch
 
 from ._lib import (SSD_BF16, SSD_F32, SSDError, ShapeT, check, lib, lib_path,  # noqa: F401
                    status_string)
+from ._block import (ssd_causal_conv1d, ssd_causal_conv1d_step, ssd_causal_conv1d_varlen,
+                     ssd_selective_scan, ssd_selective_scan_varlen, ssd_selective_step)
 
 __all__ = ["ssd_fwd", "ssd_fwd_host", "ssd_fwd_workspace_size", "ssd_fwd_plan", "ssd_fwd_check",
            "ssd_step", "ssd_fwd_cp", "ssd_cp_begin", "ssd_cp_end", "ssd_cp_record_floats",
            "ssd_gated_rmsnorm", "ssd_fwd_gated", "ssd_fwd_gated_workspace_size", "ssd_fwd_varlen", "ssd_fwd_varlen_workspace_size",
-           "ssd_fwd_varlen_check", "ssd_chunk_cumsum",
+           "ssd_fwd_varlen_check", "ssd_causal_conv1d",
+           "ssd_causal_conv1d_varlen", "ssd_causal_conv1d_step", "ssd_selective_scan",
+           "ssd_selective_scan_varlen", "ssd_selective_step", "ssd_chunk_cumsum",
            "ssd_chunk_state", "ssd_state_passing", "ssd_chunk_scan", "SSDError", "make_shape",
            "lib_path"]
 

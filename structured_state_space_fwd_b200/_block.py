@@ -1,0 +1,292 @@
+"""Binding of the operators around the layer: the short causal convolution before
+it, and the selective scan with a diagonal A. Argument marshalling only.
+
+Inputs may be slices of wider rows (a projection's output): channels contiguous,
+any non-negative strides of tokens and batch rows. Outputs are contiguous. Every
+tensor is on one device, whichever is current; a call runs on that device's
+current stream unless `stream` is given.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._lib import SSD_BF16, SSD_F32, ConvShapeT, SelectiveShapeT, StridesT, check, lib
+
+_DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+_byref = ctypes.byref
+
+
+def _in(t, name, shape, dtype, device, inner=1):
+    """An input: its shape, type and device, and its last `inner` dimensions contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is required")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        step = 1
+        for size, stride in zip(reversed(shape[len(shape) - inner:]),
+                                reversed(t.stride()[len(shape) - inner:])):
+            if size > 1 and stride != step:
+                raise ValueError(f"{name}: the last {inner} dimension(s) must be contiguous")
+            step *= size
+    return t
+
+
+def _whole(t, name, shape, dtype, device):
+    """A tensor that has to be contiguous throughout."""
+    _in(t, name, shape, dtype, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+def _first(t, name, dim):
+    """The call's first input, whose type and device the others share."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DT:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
+
+
+def _strides(t):
+    """(batch, row) strides; those of dimensions of one or no element do not matter."""
+    s, n = t.stride(), t.shape
+    return StridesT(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _call(name, device, stream, *args):
+    fn = getattr(lib(), name)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        s = torch.cuda.current_stream() if stream is None else stream
+        st = fn(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            st = fn(*args, s.cuda_stream)
+    if st:
+        check(st, name)
+
+
+def _offsets(cu_seqlens, T, device):
+    """Device offsets of a pack: a device int32 tensor as is, a host list checked and copied."""
+    if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda:
+        if (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous()
+                or cu_seqlens.numel() < 1):
+            raise ValueError("device cu_seqlens must be a contiguous 1-D int32 tensor of n_docs + 1 offsets")
+        if cu_seqlens.device != device:
+            raise ValueError(f"cu_seqlens must be on {device}, got {cu_seqlens.device}")
+        return cu_seqlens
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    from . import check_cu_seqlens
+    return torch.tensor(check_cu_seqlens(cu_seqlens, T), dtype=torch.int32).to(device)
+
+
+# ---- the short causal convolution ------------------------------------------
+
+def _conv_args(u, weight, bias, silu, split, out):
+    """Checked shape struct, outputs and whether they go back as a tuple."""
+    _first(u, "u", 3)
+    b, T, C = u.shape
+    dev = u.device
+    _in(u, "u", u.shape, u.dtype, dev)
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise ValueError("weight must be [channels, width]")
+    W = weight.shape[1]
+    _whole(weight, "weight", (C, W), torch.float32, dev)
+    if bias is not None:
+        _whole(bias, "bias", (C,), torch.float32, dev)
+    sizes = (C,) if split is None else tuple(int(c) for c in split)
+    if not 1 <= len(sizes) <= 3 or min(sizes) < 0 or sum(sizes) != C:
+        raise ValueError(f"split must be up to three sizes that add up to {C}, got {split}")
+    if out is None:
+        ys = [torch.empty((b, T, c), dtype=u.dtype, device=dev) for c in sizes]
+    else:
+        ys = [out] if split is None else list(out)
+        if len(ys) != len(sizes):
+            raise ValueError(f"out must be {len(sizes)} tensors")
+        for i, (y, c) in enumerate(zip(ys, sizes)):
+            _whole(y, f"out[{i}]", (b, T, c), u.dtype, dev)
+    pad = (0,) * (3 - len(sizes))
+    shape = ConvShapeT(b, T, C, W, (ctypes.c_int64 * 3)(*sizes, *pad), _strides(u), _DT[u.dtype],
+                       1 if silu else 0)
+    return shape, ys, [y.data_ptr() for y in ys] + [None] * len(pad)
+
+
+def _conv_states(u, W, nseq, initial_states, return_final_states, final_states):
+    size = (nseq, W - 1, u.shape[2])
+    if initial_states is not None:
+        _whole(initial_states, "initial_states", size, u.dtype, u.device)
+    if final_states is not None:
+        _whole(final_states, "final_states", size, u.dtype, u.device)
+    elif return_final_states:
+        final_states = torch.empty(size, dtype=u.dtype, device=u.device)
+    return final_states
+
+
+def _conv_result(ys, split, final_states, return_final_states):
+    y = ys[0] if split is None else tuple(ys)
+    return (y, final_states) if return_final_states else y
+
+
+def ssd_causal_conv1d(u, weight, bias=None, silu: bool = True, split=None, initial_states=None,
+                      return_final_states: bool = False, out=None, final_states=None, stream=None):
+    """Depthwise causal convolution of u [b, T, C] along T, with SiLU (Knowl 6, before the layer).
+
+    weight [C, W] fp32, W = 2..4, the last tap on the current token; bias [C] fp32 or None.
+    split: sizes of up to three parts of the channels, each returned as its own contiguous
+    tensor (a tuple), as ssd_fwd takes x, B and C; None: one tensor.
+    initial_states, final_states [b, W-1, C] in u's type: the last tokens before and of the
+    sequence. Returns y, or (y, final_states).
+    """
+    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    fin = _conv_states(u, shape.width, shape.batch, initial_states, return_final_states, final_states)
+    _call("ssd_causal_conv1d", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+          _ptr(bias), _ptr(initial_states), *yp, _ptr(fin))
+    return _conv_result(ys, split, fin, return_final_states)
+
+
+def ssd_causal_conv1d_varlen(u, weight, bias=None, cu_seqlens=None, silu: bool = True, split=None,
+                             initial_states=None, return_final_states: bool = False, out=None,
+                             final_states=None, stream=None):
+    """ssd_causal_conv1d on a pack of documents (u [1, T, C], as ssd_fwd_varlen): document k is
+    tokens cu_seqlens[k] .. cu_seqlens[k+1]-1, with its own states [n_docs, W-1, C].
+
+    cu_seqlens: a device int32 tensor [n_docs + 1] (from 0, at most T; rows behind the last
+    document are left as they were), or a host list or tensor from 0 to T (copied).
+    """
+    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    if shape.batch != 1:
+        raise ValueError("packed documents need batch 1 (u [1, T, C])")
+    cu = _offsets(cu_seqlens, shape.seqlen, u.device)
+    n = cu.numel() - 1
+    fin = _conv_states(u, shape.width, n, initial_states, return_final_states, final_states)
+    _call("ssd_causal_conv1d_varlen", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+          _ptr(bias), cu.data_ptr(), n, _ptr(initial_states), *yp, _ptr(fin))
+    return _conv_result(ys, split, fin, return_final_states)
+
+
+def ssd_causal_conv1d_step(u, weight, bias, state, silu: bool = True, split=None, out=None, stream=None):
+    """The convolution of the next tokens u [b, T, C] (or [b, C] for one) from `state`
+    [b, W-1, C], which is updated in place; returns y (a tuple with split)."""
+    one = isinstance(u, torch.Tensor) and u.dim() == 2
+    if one:
+        u = u.unsqueeze(1)
+        if out is not None:
+            out = out.unsqueeze(1) if split is None else [y.unsqueeze(1) for y in out]
+    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    _whole(state, "state", (shape.batch, shape.width - 1, shape.channels), u.dtype, u.device)
+    _call("ssd_causal_conv1d_step", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+          _ptr(bias), state.data_ptr(), *yp)
+    if one:
+        ys = [y.squeeze(1) for y in ys]
+    return ys[0] if split is None else tuple(ys)
+
+
+# ---- the selective scan ----------------------------------------------------
+
+def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
+    """Checked shape struct, the input pointers in the C order, and y."""
+    _first(u, "u", 3)
+    b, T, Dc = u.shape
+    dev, dtype = u.device, u.dtype
+    _in(u, "u", u.shape, dtype, dev)
+    if not isinstance(dt, torch.Tensor) or dt.dtype not in (torch.float32, dtype):
+        raise TypeError(f"dt must be a float32 or {dtype} tensor")
+    _in(dt, "dt", u.shape, dt.dtype, dev)
+    if not isinstance(B, torch.Tensor) or B.dim() != 4:
+        raise ValueError("B must be [batch, seqlen, ngroups, dstate]")
+    G, N = B.shape[2], B.shape[3]
+    _in(B, "B", (b, T, G, N), dtype, dev, 2)
+    _in(C, "C", (b, T, G, N), dtype, dev, 2)
+    _whole(A, "A", (Dc, N), torch.float32, dev)
+    if D is not None:
+        _whole(D, "D", (Dc,), torch.float32, dev)
+    if dt_bias is not None:
+        _whole(dt_bias, "dt_bias", (Dc,), torch.float32, dev)
+    if z is not None:
+        _in(z, "z", u.shape, dtype, dev)
+    if y is None:
+        y = torch.empty((b, T, Dc), dtype=dtype, device=dev)
+    else:
+        _whole(y, "y", (b, T, Dc), dtype, dev)
+    shape = SelectiveShapeT(b, T, Dc, G, N, _strides(u), _strides(dt),
+                            _strides(z) if z is not None else StridesT(0, 0), _strides(B), _strides(C),
+                            _DT[dtype], _DT[dt.dtype], 1 if dt_softplus else 0, 0)
+    return shape, (u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                   _ptr(z), _ptr(dt_bias)), y
+
+
+def _selective_states(u, nseq, N, initial_states, return_final_states, final_states):
+    size = (nseq, u.shape[2], N)
+    if initial_states is not None:
+        _whole(initial_states, "initial_states", size, torch.float32, u.device)
+    if final_states is not None:
+        _whole(final_states, "final_states", size, torch.float32, u.device)
+    elif return_final_states:
+        final_states = torch.empty(size, dtype=torch.float32, device=u.device)
+    return final_states
+
+
+def ssd_selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                       initial_states=None, return_final_states: bool = False, y=None,
+                       final_states=None, stream=None):
+    """The selective scan: each of u's [b, T, D] channels with its own steps and decay rates.
+
+        h_t[d, n] = exp(dt_t[d] A[d, n]) h_{t-1}[d, n] + dt_t[d] u_t[d] B_t[g, n]
+        y_t[d] = (C_t[g, :] . h_t[d, :] + D[d] u_t[d]) * SiLU(z_t[d])
+
+    dt [b, T, D] fp32 or u's type, through softplus(dt + dt_bias) with dt_softplus (dt + dt_bias
+    without); A [D, N] fp32, N up to 256; B, C [b, T, G, N]; D, dt_bias [D] fp32 or None;
+    z [b, T, D] or None (no gate). States [b, D, N] fp32. Returns y, or (y, final_states).
+    """
+    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    fin = _selective_states(u, shape.batch, shape.dstate, initial_states, return_final_states, final_states)
+    _call("ssd_selective_scan", u.device, stream, _byref(shape), *ins, _ptr(initial_states), y.data_ptr(),
+          _ptr(fin))
+    return (y, fin) if return_final_states else y
+
+
+def ssd_selective_scan_varlen(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus: bool = False,
+                              cu_seqlens=None, initial_states=None, return_final_states: bool = False,
+                              y=None, final_states=None, stream=None):
+    """ssd_selective_scan on a pack of documents (u [1, T, D]) with states [n_docs, D, N];
+    cu_seqlens as for ssd_causal_conv1d_varlen."""
+    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    if shape.batch != 1:
+        raise ValueError("packed documents need batch 1 (u [1, T, D])")
+    cu = _offsets(cu_seqlens, shape.seqlen, u.device)
+    n = cu.numel() - 1
+    fin = _selective_states(u, n, shape.dstate, initial_states, return_final_states, final_states)
+    _call("ssd_selective_scan_varlen", u.device, stream, _byref(shape), *ins, cu.data_ptr(), n,
+          _ptr(initial_states), y.data_ptr(), _ptr(fin))
+    return (y, fin) if return_final_states else y
+
+
+def ssd_selective_step(u, dt, A, B, C, D, state, z=None, dt_bias=None, dt_softplus: bool = False, y=None,
+                       stream=None):
+    """The scan of the next tokens from `state` [b, D, N] fp32, which is updated in place; returns y.
+
+    u, dt, z [b, T, D] (or [b, D] for one token), B, C [b, T, G, N] (or [b, G, N]).
+    """
+    one = isinstance(u, torch.Tensor) and u.dim() == 2
+    if one:
+        u, dt, B, C, z, y = (t.unsqueeze(1) if isinstance(t, torch.Tensor) else t for t in (u, dt, B, C, z, y))
+    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    _whole(state, "state", (shape.batch, shape.channels, shape.dstate), torch.float32, u.device)
+    _call("ssd_selective_step", u.device, stream, _byref(shape), *ins, state.data_ptr(), y.data_ptr())
+    return y.squeeze(1) if one else y

@@ -22,6 +22,26 @@ class ShapeT(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class StridesT(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("row", ctypes.c_int64)]
+
+
+class ConvShapeT(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("width", ctypes.c_int64),
+                ("out_channels", ctypes.c_int64 * 3), ("u", StridesT),
+                ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32)]
+
+
+class SelectiveShapeT(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64), ("ngroups", ctypes.c_int64),
+                ("dstate", ctypes.c_int64), ("u", StridesT), ("dt", StridesT), ("z", StridesT),
+                ("B", StridesT), ("C", StridesT), ("dtype", ctypes.c_int32),
+                ("dt_dtype", ctypes.c_int32), ("dt_softplus", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class SSDError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str = ""):
         self.status = status
@@ -66,6 +86,14 @@ _SIGS = {
                    + [ctypes.c_size_t, _VP], ctypes.c_int),
     "ssd_gated_rmsnorm": ([ctypes.POINTER(ShapeT), _VP, _VP, _VP, ctypes.c_int64, ctypes.c_float,
                            _VP, _VP], ctypes.c_int),
+    "ssd_causal_conv1d": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 9, ctypes.c_int),
+    "ssd_causal_conv1d_varlen": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 4 + [ctypes.c_int64] + [_VP] * 6,
+                                 ctypes.c_int),
+    "ssd_causal_conv1d_step": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 8, ctypes.c_int),
+    "ssd_selective_scan": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 12, ctypes.c_int),
+    "ssd_selective_scan_varlen": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 9 + [ctypes.c_int64]
+                                  + [_VP] * 4, ctypes.c_int),
+    "ssd_selective_step": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 11, ctypes.c_int),
     "ssd_chunk_cumsum": ([ctypes.POINTER(ShapeT), _VP, _VP, _VP, _VP], ctypes.c_int),
     "ssd_chunk_state": ([ctypes.POINTER(ShapeT)] + [_VP] * 6, ctypes.c_int),
     "ssd_state_passing": ([ctypes.POINTER(ShapeT)] + [_VP] * 6, ctypes.c_int),

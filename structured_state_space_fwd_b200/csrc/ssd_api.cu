@@ -56,18 +56,9 @@ ssd_status_t check_shape(const ssd_shape_t* s) {
 
 size_t elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
 
-struct Range {
-    const void* p;
-    size_t bytes;
-};
-
-bool overlaps(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+using ssd::aligned;
+using ssd::overlaps;
+using ssd::Range;
 
 struct Sizes {
     size_t x, dt, hv, bc, st, cs, chunk_states;

@@ -1,0 +1,100 @@
+// Device helpers of the operators around the layer: typed 1-, 4- and 8-element
+// loads and stores, SiLU and softplus in fp32.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace ssd {
+
+// VW consecutive elements as they lie in memory: 16 bytes, or one element.
+template <typename E, int VW>
+struct Pack {
+    using T = uint4;
+};
+template <typename E>
+struct Pack<E, 1> {
+    using T = E;
+};
+
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_elem(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[8]) {
+    v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+    v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+}
+__device__ __forceinline__ void unpack(const uint4& q, float (&v)[4]) {
+    v[0] = __uint_as_float(q.x); v[1] = __uint_as_float(q.y);
+    v[2] = __uint_as_float(q.z); v[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack(float q, float (&v)[1]) { v[0] = q; }
+__device__ __forceinline__ void unpack(__nv_bfloat16 q, float (&v)[1]) { v[0] = __bfloat162float(q); }
+
+__device__ __forceinline__ void pack(const float (&v)[8], uint4& q) {
+    q = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void pack(const float (&v)[4], uint4& q) {
+    q = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ void pack(const float (&v)[1], float& q) { q = v[0]; }
+__device__ __forceinline__ void pack(const float (&v)[1], __nv_bfloat16& q) { q = __float2bfloat16_rn(v[0]); }
+
+template <typename P>
+__device__ __forceinline__ P zero_pack() {
+    if constexpr (sizeof(P) == 16) {
+        return make_uint4(0, 0, 0, 0);
+    } else {
+        return P(0.f);
+    }
+}
+
+// 2^x and 1/x on the special-function unit (2 and 1 ulp).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// v / (1 + exp(-v)): 0 for very negative v (the divisor is inf), NaN for -inf as the formula.
+__device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
+
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]. With s = e / (2 + e) in
+// (0, 1/3], log1p(e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): the series to s^15 leaves
+// a relative error below (1/9)^8 / 17 = 1.4e-9, so small steps keep their full precision, which
+// log(1 + e) would lose. The exponent's product with log2 e is carried in two floats: at
+// v = -12 its rounding alone would cost 2^-21 of the result.
+__device__ __forceinline__ float softplus(float v) {
+    float m = -fabsf(v);
+    m = m < -126.f ? -126.f : m;      // e is 0 there; keeps infinities finite, and NaN NaN
+    const float hi = m * kLog2e;
+    const float lo = fmaf(m, kLog2e, -hi) + m * 1.92596299e-8f;   // log2 e - float(log2 e)
+    const float e = ex2(hi) * fmaf(lo, 0.6931471805599453f, 1.f);
+    const float s = e * rcp(2.f + e);
+    const float q = s * s;
+    float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
+    p = fmaf(p, q, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    return fmaxf(v, 0.f) + fmaf(2.f * s * q, p, 2.f * s);
+}
+
+}  // namespace ssd

@@ -137,6 +137,59 @@ cudaError_t launch_cp_fold(const Dims& d, const float* records, int64_t rec_floa
 cudaError_t launch_gated_rmsnorm(const Dims& d, const void* y, const void* z, const float* w,
                                  int64_t group_size, float eps, void* out, cudaStream_t st);
 
+// Short causal convolution (ssd_conv.cu). cu null: `b` sequences of T tokens, else nseq
+// documents of one pack of T tokens (b == 1).
+struct ConvArgs {
+    int64_t b, T, C, nseq;
+    int64_t oc[3];             // channels of the three outputs
+    int64_t ub, ur;            // batch and token strides of u
+    int W, dtype, silu;
+    const void* u;
+    const float* weight;
+    const float* bias;
+    const int* cu;
+    const void* init;          // [nseq, W-1, C] or null
+    void* y[3];
+    void* final_states;        // [nseq, W-1, C] or null
+};
+cudaError_t launch_conv(const ConvArgs& a, cudaStream_t st);
+// `state` [b, W-1, C] updated in place; a.init, a.final_states and a.cu are not used
+cudaError_t launch_conv_step(const ConvArgs& a, void* state, cudaStream_t st);
+
+// Selective scan with a diagonal A (ssd_selective.cu). cu as for ConvArgs. init and fin may be the
+// same memory (the decoding form).
+struct SelectiveArgs {
+    int64_t b, T, D, G, N, nseq;
+    ssd_strides_t us, dts, zs, Bs, Cs;
+    int dtype, dt_dtype, softplus;
+    const void* u;
+    const void* dt;
+    const float* A;
+    const void* B;
+    const void* C;
+    const float* Dskip;
+    const void* z;
+    const float* dt_bias;
+    const int* cu;
+    const float* init;         // [nseq, D, N] or null
+    void* y;
+    float* fin;                // [nseq, D, N] or null
+};
+cudaError_t launch_selective_scan(const SelectiveArgs& a, cudaStream_t st);
+cudaError_t launch_selective_step(const SelectiveArgs& a, cudaStream_t st);
+
+// A region of caller memory, for the checks that outputs overlap nothing else.
+struct Range {
+    const void* p;
+    size_t bytes;
+};
+inline bool overlaps(Range a, Range b) {
+    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
+    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
+}
+inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
 // Sets the message ssd_last_error_detail() returns on the calling host thread.
 void set_error_detail(const char* msg);
 
