@@ -76,10 +76,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
 
 // log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]. With s = e / (2 + e) in
-// (0, 1/3], log1p(e) = 2 atanh(s) = 2 (s + s^3/3 + s^5/5 + ...): the series to s^15 leaves
-// a relative error below (1/9)^8 / 17 = 1.4e-9, so small steps keep their full precision, which
-// log(1 + e) would lose. The exponent's product with log2 e is carried in two floats: at
-// v = -12 its rounding alone would cost 2^-21 of the result.
+// (0, 1/3], log1p(e) = 2 atanh(s) = 2 s (1 + q P(q)), q = s^2 in (0, 1/9]; P interpolates
+// (atanh(sqrt q) / sqrt q - 1) / q in four Chebyshev nodes, which leaves a relative error of
+// 1.6e-8. So small steps keep their full precision, which log(1 + e) would lose. The exponent's
+// product with log2 e is carried in two floats: at v = -12 its rounding alone would cost 2^-21.
 __device__ __forceinline__ float softplus(float v) {
     float m = -fabsf(v);
     m = m < -126.f ? -126.f : m;      // e is 0 there; keeps infinities finite, and NaN NaN
@@ -88,13 +88,10 @@ __device__ __forceinline__ float softplus(float v) {
     const float e = ex2(hi) * fmaf(lo, 0.6931471805599453f, 1.f);
     const float s = e * rcp(2.f + e);
     const float q = s * s;
-    float p = fmaf(q, 1.f / 15.f, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    return fmaxf(v, 0.f) + fmaf(2.f * s * q, p, 2.f * s);
+    float p = fmaf(q, 0.1342574954f, 0.1411830932f);
+    p = fmaf(p, q, 0.2000378072f);
+    p = fmaf(p, q, 0.3333331943f);
+    return fmaf(2.f * s * q, p, fmaf(2.f, s, fmaxf(v, 0.f)));
 }
 
 }  // namespace ssd
