@@ -406,7 +406,7 @@ SSD_API ssd_status_t ssd_causal_conv1d_step(const ssd_conv_shape_t* shape, const
  */
 typedef struct {
     int64_t batch;        /* b >= 0                                          */
-    int64_t seqlen;       /* T >= 0                                          */
+    int64_t seqlen;       /* T >= 0, at most 2^31 - 2^16                     */
     int64_t channels;     /* D >= 1                                          */
     int64_t ngroups;      /* G >= 1, divides D                               */
     int64_t dstate;       /* N in [1, 256]                                   */

@@ -75,23 +75,27 @@ constexpr float kLog2e = 1.4426950408889634f;
 // v / (1 + exp(-v)): 0 for very negative v (the divisor is inf), NaN for -inf as the formula.
 __device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
 
-// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1]. With s = e / (2 + e) in
-// (0, 1/3], log1p(e) = 2 atanh(s) = 2 s (1 + q P(q)), q = s^2 in (0, 1/9]; P interpolates
-// (atanh(sqrt q) / sqrt q - 1) / q in four Chebyshev nodes, which leaves a relative error of
-// 1.6e-8. So small steps keep their full precision, which log(1 + e) would lose. The exponent's
-// product with log2 e is carried in two floats: at v = -12 its rounding alone would cost 2^-21.
-__device__ __forceinline__ float softplus(float v) {
-    float m = -fabsf(v);
-    m = m < -126.f ? -126.f : m;      // e is 0 there; keeps infinities finite, and NaN NaN
-    const float hi = m * kLog2e;
-    const float lo = fmaf(m, kLog2e, -hi) + m * 1.92596299e-8f;   // log2 e - float(log2 e)
-    const float e = ex2(hi) * fmaf(lo, 0.6931471805599453f, 1.f);
-    const float s = e * rcp(2.f + e);
-    const float q = s * s;
-    float p = fmaf(q, 0.1342574954f, 0.1411830932f);
-    p = fmaf(p, q, 0.2000378072f);
-    p = fmaf(p, q, 0.3333331943f);
-    return fmaf(2.f * s * q, p, fmaf(2.f, s, fmaxf(v, 0.f)));
+// log(1 + exp(v)) = max(v, 0) + log1p(e), e = exp(-|v|) in (0, 1], of two values. With
+// s = e / (2 + e) in (0, 1/3], log1p(e) = 2 atanh(s) = 2 s (1 + q P(q)), q = s^2 in (0, 1/9]; P
+// interpolates (atanh(sqrt q) / sqrt q - 1) / q in four Chebyshev nodes, which leaves a relative
+// error of 1.6e-8. So small steps keep their precision, which log(1 + e) would lose; the rounding
+// of the exponent v log2(e) moves e by at most 2^-24 |v|.
+__device__ __forceinline__ float2 softplus2(float2 v) {
+    float2 m = make_float2(-fabsf(v.x), -fabsf(v.y));
+    m.x = m.x < -126.f ? -126.f : m.x;      // e is 0 there; keeps infinities finite, and NaN NaN
+    m.y = m.y < -126.f ? -126.f : m.y;
+    const float2 one = make_float2(1.f, 1.f), two = make_float2(2.f, 2.f);
+    float2 e = __fmul2_rn(m, make_float2(kLog2e, kLog2e));
+    e = make_float2(ex2(e.x), ex2(e.y));
+    const float2 d = __fadd2_rn(e, two);
+    const float2 s = __fmul2_rn(e, make_float2(rcp(d.x), rcp(d.y)));
+    const float2 q = __fmul2_rn(s, s);
+    float2 p = __ffma2_rn(q, make_float2(0.1342574954f, 0.1342574954f), make_float2(0.1411830932f, 0.1411830932f));
+    p = __ffma2_rn(p, q, make_float2(0.2000378072f, 0.2000378072f));
+    p = __ffma2_rn(p, q, make_float2(0.3333331943f, 0.3333331943f));
+    p = __ffma2_rn(p, q, one);
+    return __ffma2_rn(__fmul2_rn(s, two), p, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
+__device__ __forceinline__ float softplus(float v) { return softplus2(make_float2(v, v)).x; }
 
 }  // namespace ssd

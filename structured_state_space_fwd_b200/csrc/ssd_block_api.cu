@@ -17,6 +17,7 @@ using ssd::Range;
 
 constexpr int64_t kMaxState = 256;
 constexpr int64_t kMaxDocs = 1 << 24;
+constexpr int64_t kMaxTokens = 0x7fff0000;   // token counts of the scan's kernels are 32-bit
 constexpr double kMaxElems = 4.0e15;      // keeps every element index well inside int64
 
 size_t elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
@@ -119,7 +120,7 @@ ssd_status_t check_selective_shape(const ssd_selective_shape_t* s) {
     if (!dtype_ok(s->dtype) || !dtype_ok(s->dt_dtype) || (s->dt_dtype != SSD_F32 && s->dt_dtype != s->dtype) ||
         (s->dt_softplus != 0 && s->dt_softplus != 1))
         return SSD_ERR_INVALID_ARG;
-    if (s->dstate > kMaxState) return SSD_ERR_UNSUPPORTED;
+    if (s->dstate > kMaxState || s->seqlen > kMaxTokens) return SSD_ERR_UNSUPPORTED;
     if ((double)s->batch * (double)s->seqlen * (double)s->channels > kMaxElems ||
         (double)s->batch * (double)s->seqlen * (double)s->ngroups * (double)s->dstate > kMaxElems ||
         (double)s->batch * (double)s->channels * (double)s->dstate > kMaxElems)

@@ -8,20 +8,22 @@
 //
 // What bounds it: one exponential for each (token, channel, state) on the special-function
 // unit, 16 a clock and SM (with 16 states: 16 + 4 for softplus and SiLU against 8 bytes of HBM
-// traffic in bf16, 3.6 times the time of the bytes), and beside it about as many issue slots.
+// traffic in bf16, 3.6 times the time of the bytes), and beside it nearly as many issue slots.
 // So every exponential is computed once, also where the sequence is cut.
 //
-// Layout: a warp takes 32 / SL channels, SL lanes a channel, 4 states a lane (more than 4 SL
-// states in blocks), and kTok tokens at a time: its tokens' inputs arrive by asynchronous copies
-// a tile ahead, softplus and dt u are computed once per (token, channel), and each lane then runs
-// its 4 states through the tokens with packed fp32x2 arithmetic. The lanes' parts of y are summed
-// by exchanges that leave every lane kTok / SL tokens.
+// Layout: a warp takes 64 / SL channels, SL lanes for a pair of channels, 4 states a lane (more
+// than 4 SL states in blocks), and K tokens at a time. Its tokens' inputs arrive by asynchronous
+// copies a tile ahead; softplus and dt u are computed once per (token, channel); then each lane
+// runs its 2 x 4 states through the tokens with packed fp32x2 arithmetic. Two channels a lane
+// halve the reads of B and C from shared memory, whose port otherwise binds before the
+// exponentials. The lanes' parts of y are summed by exchanges that leave every lane K / SL tokens.
 //
-// The cut (kSplit): where there are few channels, the warps of a CTA take consecutive runs of
-// kTok tokens of the same channels. Each runs from a state of zero and keeps, per token and
-// state, C_t times the product of its decays so far: the state entering the run, the fold of the
-// runs before it, h <- P h + h_local, then adds sum_n (C_t prod a)[n] h_in[n] to each y_t, at two
-// packed operations per pair and no second exponential.
+// The cut (kSplit): where there are few channels, the warps of a CTA take consecutive runs of K
+// tokens of the same channels. Each runs from a state of zero and keeps, per token and state, C_t
+// times the product of its decays so far. The entering states go from warp to warp as a chain,
+// h <- (prod a) h + h_local, over shared memory and a named barrier of the two warps, so that the
+// warps stay at different phases; with its entering state a warp adds sum_n (C_t prod a)[n] h[n]
+// to each y_t, at two packed operations per pair of states and no second exponential.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,8 +35,6 @@
 namespace ssd {
 namespace {
 
-constexpr int kTok = 16;         // tokens of a warp's tile
-constexpr int kMaxWarps = 8;
 
 struct ScanParams {
     SelectiveArgs a;
@@ -42,6 +42,7 @@ struct ScanParams {
     int64_t cblocks;             // channel blocks of a group
     int nblocks;                 // state blocks
     bool rows16, bc16;           // u, dt, z (B, C) take 16-byte copies
+    bool y_pairs;                // y takes stores of two channels
 };
 
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool ok) {
@@ -59,26 +60,52 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// Named barriers of two warps: the one that hands over goes on (or waits too), the other waits. The
+// ids are immediates, so that a CTA reserves no more barriers than it uses.
+template <int kIds>
+__device__ __forceinline__ void pair_arrive(int id) {
+#define SSD_ARRIVE(i) \
+    if constexpr (i < kIds) { if (id == i) asm volatile("bar.arrive " #i ", 64;" ::: "memory"); }
+    SSD_ARRIVE(0) SSD_ARRIVE(1) SSD_ARRIVE(2) SSD_ARRIVE(3) SSD_ARRIVE(4) SSD_ARRIVE(5) SSD_ARRIVE(6) SSD_ARRIVE(7)
+    SSD_ARRIVE(8) SSD_ARRIVE(9) SSD_ARRIVE(10) SSD_ARRIVE(11) SSD_ARRIVE(12) SSD_ARRIVE(13) SSD_ARRIVE(14)
+    SSD_ARRIVE(15)
+#undef SSD_ARRIVE
+}
+template <int kIds>
+__device__ __forceinline__ void pair_wait(int id) {
+#define SSD_WAIT(i) \
+    if constexpr (i < kIds) { if (id == i) asm volatile("bar.sync " #i ", 64;" ::: "memory"); }
+    SSD_WAIT(0) SSD_WAIT(1) SSD_WAIT(2) SSD_WAIT(3) SSD_WAIT(4) SSD_WAIT(5) SSD_WAIT(6) SSD_WAIT(7)
+    SSD_WAIT(8) SSD_WAIT(9) SSD_WAIT(10) SSD_WAIT(11) SSD_WAIT(12) SSD_WAIT(13) SSD_WAIT(14) SSD_WAIT(15)
+#undef SSD_WAIT
+}
 
-// kTok rows of W elements from src (row stride `row`) to dst [kTok][W], zeros where the token is not
-// below `tokens` or the column not below `cols`. wide: 16-byte pieces (a piece is then inside or
+// Copies K rows of W elements, row stride `row`, to shared memory [K][W], zeros where the row is not
+// below `rows` or the column not below `cols`. wide: in 16-byte pieces (a piece is then inside or
 // outside as a whole).
-template <int W, typename E>
-__device__ __forceinline__ void stage(E* dst, const E* src, int64_t row, int tokens, int cols, bool wide, int lane) {
-    constexpr int V = 16 / sizeof(E);
+template <int K, int W, typename E>
+__device__ __forceinline__ void stage(E* dst, const E* src, int64_t row, int rows, int cols, int lane, bool wide) {
+    constexpr int V = 16 / sizeof(E), P = W >= V ? W / V : 1, kPieces = (K * P + 31) / 32;
     if (W >= V && wide) {
-        constexpr int P = W >= V ? W / V : 1;
+        const int k0 = lane / P, c = (lane % P) * V;
+        const E* from = src + k0 * row + c;
+        if (rows == K && cols >= W) {
 #pragma unroll
-        for (int i = 0; i < (kTok * P + 31) / 32; ++i) {
-            const int idx = lane + 32 * i, k = idx / P, c = (idx % P) * V;
-            const bool ok = k < tokens && c < cols;
-            if (kTok * P % 32 == 0 || idx < kTok * P) copy16(dst + k * W + c, ok ? src + k * row + c : src, ok);
+            for (int i = 0; i < kPieces; ++i)
+                if (K * P % 32 == 0 || k0 < K) copy16(dst + (k0 + i * (32 / P)) * W + c, from + i * (32 / P) * row, true);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int k = k0 + i * (32 / P);
+                const bool ok = k < rows && c < cols;
+                if (K * P % 32 == 0 || k < K) copy16(dst + k * W + c, ok ? from + i * (32 / P) * row : src, ok);
+            }
         }
     } else {
-#pragma unroll 4
-        for (int idx = lane; idx < kTok * W; idx += 32) {
+#pragma unroll 2
+        for (int idx = lane; idx < K * W; idx += 32) {
             const int k = idx / W, c = idx % W;
-            const bool ok = k < tokens && c < cols;
+            const bool ok = k < rows && c < cols;
             if constexpr (sizeof(E) == 4) {
                 copy4(dst + idx, ok ? src + k * row + c : src, ok);
             } else {
@@ -89,310 +116,382 @@ __device__ __forceinline__ void stage(E* dst, const E* src, int64_t row, int tok
 }
 
 // A warp's shared memory: two stages of raw inputs, the tile's (dt, dt u), and B, C in fp32.
-template <typename E, typename Td, int SL>
+template <typename E, typename Td, int SL, int K>
 struct WarpMem {
-    static constexpr int CH = 32 / SL, NS = 4 * SL;
-    alignas(16) E u[2][kTok][CH];
-    alignas(16) E z[2][kTok][CH];
-    alignas(16) Td dt[2][kTok][CH];
-    alignas(16) E B[2][kTok][NS];
-    alignas(16) E C[2][kTok][NS];
-    alignas(16) float2 s[kTok][CH];
-    alignas(16) float Bf[sizeof(E) == 2 ? kTok : 1][NS];
-    alignas(16) float Cf[sizeof(E) == 2 ? kTok : 1][NS];
+    static constexpr int CH = 64 / SL, NS = 4 * SL;
+    alignas(16) E u[2][K][CH];
+    alignas(16) E z[2][K][CH];
+    alignas(16) Td dt[2][K][CH];
+    alignas(16) E B[2][K][NS];
+    alignas(16) E C[2][K][NS];
+    alignas(16) float4 s[K][CH / 2];          // dt, dt u of two channels
+    alignas(16) float Bf[sizeof(E) == 2 ? K : 1][NS];
+    alignas(16) float Cf[sizeof(E) == 2 ? K : 1][NS];
 };
 
-template <int NS>
+// Two neighbouring elements.
+__device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    return make_float2(bf16_lo(v), bf16_hi(v));
+}
+__device__ __forceinline__ void store_pair(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
+    *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+template <int K, int NS>
 __device__ __forceinline__ void widen(float (*dst)[NS], const __nv_bfloat16 (*src)[NS], int lane) {
-    // kTok * NS values, 8 a lane and round
 #pragma unroll
-    for (int i = 0; i < (kTok * NS + 255) / 256; ++i) {
-        const int at = (lane + 32 * i) * 8;
-        if (kTok * NS % 256 == 0 || at < kTok * NS) {
-            float v[8];
-            unpack(*reinterpret_cast<const uint4*>(&src[0][0] + at), v);
-            float4* d = reinterpret_cast<float4*>(&dst[0][0] + at);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    for (int i = 0; i < (K * NS + 127) / 128; ++i) {
+        const int at = (lane + 32 * i) * 4;
+        if (K * NS % 128 == 0 || at < K * NS) {
+            const uint2 q = *reinterpret_cast<const uint2*>(&src[0][0] + at);
+            *reinterpret_cast<float4*>(&dst[0][0] + at) =
+                make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
         }
     }
 }
 
-template <typename E, typename Td, int SL, bool kSplit>
-__global__ void __launch_bounds__(kMaxWarps * 32, 2) scan_kernel(const ScanParams p) {
-    constexpr int CH = 32 / SL, NS = 4 * SL;
-    using Mem = WarpMem<E, Td, SL>;
+// 2 x 4 states of a lane (or their decays): [channel of the pair][pair of states]
+struct States {
+    float2 v[2][2];
+    __device__ __forceinline__ void fill(float x) {
+        v[0][0] = v[0][1] = v[1][0] = v[1][1] = both(x);
+    }
+    __device__ __forceinline__ void load(const float4* p) {
+        const float4 a = p[0], b = p[32];
+        v[0][0] = make_float2(a.x, a.y); v[0][1] = make_float2(a.z, a.w);
+        v[1][0] = make_float2(b.x, b.y); v[1][1] = make_float2(b.z, b.w);
+    }
+    __device__ __forceinline__ void store(float4* p) const {
+        p[0] = make_float4(v[0][0].x, v[0][0].y, v[0][1].x, v[0][1].y);
+        p[32] = make_float4(v[1][0].x, v[1][0].y, v[1][1].x, v[1][1].y);
+    }
+};
+
+// Forms of the kernel. kAlternate: the two warps of a CTA take the tiles of one unit (sequence, block
+// of channels) in turn, and while one runs the states through its tile the other prepares its next
+// and finishes its last. kCut4, 8, 16: the cut form with that many warps.
+enum Form { kAlternate = 2, kCut4 = 4, kCut8 = 8, kCut16 = 16 };
+__host__ __device__ constexpr int form_warps(Form f) { return (int)f; }
+// resident CTAs per SM that the registers are capped for
+__host__ __device__ constexpr int form_ctas(Form f) { return f == kAlternate ? 9 : 16 / (int)f; }
+// tokens of a warp's tile: the cut form keeps 8 floats a token in registers, and with few states a
+// lane's rows are wide
+__host__ __device__ constexpr int form_tokens(Form f, int SL) { return f != kAlternate || SL < 4 ? 8 : 16; }
+
+template <typename E, typename Td, int SL, Form F>
+__global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(const __grid_constant__ ScanParams p) {
+    constexpr bool kCut = F != kAlternate;
+    constexpr int W = form_warps(F), K = form_tokens(F, SL);
+    constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
+    using Mem = WarpMem<E, Td, SL, K>;
     extern __shared__ __align__(16) unsigned char smem[];
     const SelectiveArgs& a = p.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int ch = lane % CH, j = lane / CH;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int cp = lane % CL, j = lane / CL;             // pair of channels, states 4 j ..
     const int NB = p.nblocks;
     Mem& m = reinterpret_cast<Mem*>(smem)[warp];
-    // split: per run and parity, local states and decays; then the carried states, by parity and state block.
-    // Not split: each warp's own carried states.
-    float4* const exchange = reinterpret_cast<float4*>(smem + warps * sizeof(Mem));
-    float4* const carry = exchange + (kSplit ? 4 * warps * 32 : warp * NB * 32);
+    // the states entering the next tile (cut: the next W tiles), by state block; cut: two slots a warp
+    // for what its predecessor hands over
+    float4* const carry = reinterpret_cast<float4*>(smem + W * sizeof(Mem));
+    float4* const slots = carry + NB * 64;
 
-    // the warp's sequence, group and channels
-    int64_t unit = blockIdx.x;
-    if constexpr (!kSplit) unit = unit * warps + warp;
-    const int64_t per_seq = p.cblocks * a.G;
+    const int64_t unit = blockIdx.x, per_seq = p.cblocks * a.G;
     const int64_t seq = unit / per_seq, g = unit % per_seq / p.cblocks, c0 = unit % p.cblocks * CH;
-    if (!kSplit && seq >= a.nseq) return;
     const int64_t b = a.cu ? 0 : seq;
-    int64_t t0 = 0, t1 = a.T;
+    int t0 = 0, t1 = (int)a.T;
     if (a.cu) {
-        t0 = min((int64_t)max(a.cu[seq], 0), a.T);
-        t1 = min((int64_t)max(a.cu[seq + 1], 0), a.T);
+        t0 = min(max(a.cu[seq], 0), t1);
+        t1 = min(max(a.cu[seq + 1], 0), t1);
     }
     const int cols = (int)min(p.per - c0, (int64_t)CH);
     const int64_t d0 = g * p.per + c0;
-    const int64_t d = d0 + (ch < cols ? ch : 0);
     const int N = (int)a.N;
-    const E* const u = static_cast<const E*>(a.u) + b * a.us.batch + d0;
-    const Td* const dt = static_cast<const Td*>(a.dt) + b * a.dts.batch + d0;
-    const E* const z = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d0 : nullptr;
-    const E* const B = static_cast<const E*>(a.B) + b * a.Bs.batch + g * N;
-    const E* const C = static_cast<const E*>(a.C) + b * a.Cs.batch + g * N;
-    E* const y = static_cast<E*>(a.y) + b * a.T * a.D + d0;
-    const float skip = a.Dskip ? a.Dskip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+    const bool in0 = 2 * cp < cols, in1 = 2 * cp + 1 < cols;
+    const int64_t da = d0 + (in0 ? 2 * cp : 0), db = d0 + (in1 ? 2 * cp + 1 : 0);   // the lane's channels
+    const float2 skip = a.Dskip ? make_float2(a.Dskip[da], a.Dskip[db]) : both(0.f);
+    const float2 bias = a.dt_bias ? make_float2(a.dt_bias[da], a.dt_bias[db]) : both(0.f);
 
-    const int64_t state0 = (seq * a.D + d) * N;
-    if (!kSplit || warp == 0) {
-        for (int nb = 0; nb < NB; ++nb) {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = nb * NS + j * 4 + i;
-                v[i] = a.init && n < N ? a.init[state0 + n] : 0.f;
-            }
-            carry[nb * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
-        }
-    }
-
-    const int64_t tile = kSplit ? (int64_t)warps * kTok : kTok;
-    const int64_t ntiles = t1 > t0 ? (t1 - t0 + tile - 1) / tile : 0;
-    const int64_t iters = ntiles * NB;
-    auto tokens_at = [&](int64_t it, int64_t* t) {     // the warp's first token of iteration it, and how many
-        *t = t0 + it * tile + (kSplit ? warp * kTok : 0);
-        const int64_t left = t1 - *t;
-        return (int)(left < 0 ? 0 : (left > kTok ? kTok : left));
-    };
-    auto issue = [&](int64_t it, int nb) {
-        int64_t t;
-        const int n = tokens_at(it, &t);
-        if (n > 0) {
-            if (nb == 0) {
-                const int s = (int)(it & 1);
-                stage<CH>(&m.u[s][0][0], u + t * a.us.row, a.us.row, n, cols, p.rows16, lane);
-                stage<CH>(&m.dt[s][0][0], dt + t * a.dts.row, a.dts.row, n, cols, p.rows16, lane);
-                if (z) stage<CH>(&m.z[s][0][0], z + t * a.zs.row, a.zs.row, n, cols, p.rows16, lane);
-            }
-            const int s = (int)((it * NB + nb) & 1);
-            stage<NS>(&m.B[s][0][0], B + t * a.Bs.row + nb * NS, a.Bs.row, n, N - nb * NS, p.bc16, lane);
-            stage<NS>(&m.C[s][0][0], C + t * a.Cs.row + nb * NS, a.Cs.row, n, N - nb * NS, p.bc16, lane);
-        }
-        copy_commit();
-    };
-
-    float yv[kTok];
-    float2 A0, A1;
-    auto rates = [&](int nb) {
+    auto row_of = [&](const float* base, int64_t d, int nb, float scale, float2& lo, float2& hi) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int n = nb * NS + j * 4 + i;
-            v[i] = n < N ? a.A[d * N + n] * kLog2e : 0.f;
+            v[i] = base && n < N ? base[d * N + n] * scale : 0.f;
         }
-        A0 = make_float2(v[0], v[1]);
-        A1 = make_float2(v[2], v[3]);
+        lo = make_float2(v[0], v[1]);
+        hi = make_float2(v[2], v[3]);
     };
-    if (NB == 1) rates(0);
-    if (iters > 0) issue(0, 0);
-    int64_t it = 0;
-    int nb = 0;
-    for (int64_t i = 0; i < iters; ++i) {
-        __syncwarp();                                   // the stage that is filled next has been read
-        const int nb1 = nb + 1 == NB ? 0 : nb + 1;
-        const int64_t it1 = nb1 == 0 ? it + 1 : it;
-        if (i + 1 < iters) issue(it1, nb1);
-        else copy_commit();
-        copy_wait<1>();
-        __syncwarp();
-        int64_t t;
-        const int n = tokens_at(it, &t);
-        const int sr = (int)(it & 1), sb = (int)(i & 1);
-        if (nb == 0) {
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) yv[k] = 0.f;
+    if (warp == 0) {
+        const float* const init = a.init ? a.init + seq * a.D * N : nullptr;
+        for (int nb = 0; nb < NB; ++nb) {
+            States h;
+            row_of(init, da, nb, 1.f, h.v[0][0], h.v[0][1]);
+            row_of(init, db, nb, 1.f, h.v[1][0], h.v[1][1]);
+            h.store(carry + nb * 64 + lane);
         }
-        if (NB > 1) rates(nb);
-        float4 h = make_float4(0.f, 0.f, 0.f, 0.f);
-        float4 decay = make_float4(1.f, 1.f, 1.f, 1.f);
-        float2 gc[kSplit ? kTok : 1][2];
-        if (!kSplit) h = carry[nb * 32 + lane];
+    }
+
+    const E* const ub = static_cast<const E*>(a.u) + b * a.us.batch + d0;
+    const Td* const dtb = static_cast<const Td*>(a.dt) + b * a.dts.batch + d0;
+    const E* const zb = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d0 : nullptr;
+    const E* const Bb = static_cast<const E*>(a.B) + b * a.Bs.batch + g * N;
+    const E* const Cb = static_cast<const E*>(a.C) + b * a.Cs.batch + g * N;
+    // the copies of the tile at token t, state block nb; u, dt, z (stage sr) with the first block
+    auto issue = [&](int t, int nb, int sr, int sb) {
+        const int n = min(t1 - t, K);
         if (n > 0) {
             if (nb == 0) {
-                // once per (token, channel): the step and dt u; past the end both are 0, which
-                // leaves the state as it is
-#pragma unroll
-                for (int q = 0; q < kTok / SL; ++q) {
-                    const int k = q * SL + j;
-                    float v = to_float(m.dt[sr][k][ch]) + bias;
-                    if (a.softplus) v = softplus(v);
-                    v = k < n ? v : 0.f;
-                    m.s[k][ch] = make_float2(v, v * to_float(m.u[sr][k][ch]));
-                }
+                stage<K, CH>(&m.u[sr][0][0], ub + t * a.us.row, a.us.row, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.dt[sr][0][0], dtb + t * a.dts.row, a.dts.row, n, cols, lane, p.rows16);
+                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + t * a.zs.row, a.zs.row, n, cols, lane, p.rows16);
             }
-            if constexpr (sizeof(E) == 2) {
-                widen<NS>(m.Bf, m.B[sb], lane);
-                widen<NS>(m.Cf, m.C[sb], lane);
-            }
+            stage<K, NS>(&m.B[sb][0][0], Bb + t * a.Bs.row + nb * NS, a.Bs.row, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.C[sb][0][0], Cb + t * a.Cs.row + nb * NS, a.Cs.row, n, N - nb * NS, lane, p.bc16);
+        }
+        copy_commit();
+    };
+
+    // Cut: all warps take part in every round of W tiles, those past the end too, which pass the
+    // states on. Alternating: a warp takes every second tile.
+    const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
+    const int rounds = (tiles + W - 1) / W;
+    const int mine = kCut ? rounds : (tiles - warp + W - 1) / W;
+    float2 yv[K];
+    States A;
+    auto rates = [&](int nb) {
+        row_of(a.A, da, nb, kLog2e, A.v[0][0], A.v[0][1]);
+        row_of(a.A, db, nb, kLog2e, A.v[1][0], A.v[1][1]);
+    };
+    if (NB == 1) rates(0);
+    int t = t0 + warp * K, sr = 0, sb = 0;
+    if (mine > 0) issue(t, 0, 0, 0);
+    for (int it = 0; it < mine; ++it, t += W * K, sr ^= 1) {
+        const int n = min(t1 - t, K);
+        for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
+            __syncwarp();                                // the stage that is filled next has been read
+            if (nb + 1 < NB)
+                issue(t, nb + 1, sr ^ 1, sb ^ 1);
+            else if (it + 1 < mine)
+                issue(t + W * K, 0, sr ^ 1, sb ^ 1);
+            else
+                copy_commit();
+            copy_wait<1>();
             __syncwarp();
-            const float* Bt;
-            const float* Ct;
-            if constexpr (sizeof(E) == 2) {
-                Bt = &m.Bf[0][0];
-                Ct = &m.Cf[0][0];
-            } else {
-                Bt = &m.B[sb][0][0];
-                Ct = &m.C[sb][0][0];
-            }
-            float2 h0 = make_float2(h.x, h.y), h1 = make_float2(h.z, h.w);
-            float2 p0 = make_float2(1.f, 1.f), p1 = p0;
-#pragma unroll
-            for (int k = 0; k < kTok; ++k) {
-                const float2 s = m.s[k][ch];
-                const float4 Bk = *reinterpret_cast<const float4*>(Bt + k * NS + j * 4);
-                const float4 Ck = *reinterpret_cast<const float4*>(Ct + k * NS + j * 4);
-                const float2 st = make_float2(s.x, s.x), su = make_float2(s.y, s.y);
-                float2 a0 = __fmul2_rn(st, A0), a1 = __fmul2_rn(st, A1);
-                a0 = make_float2(ex2(a0.x), ex2(a0.y));
-                a1 = make_float2(ex2(a1.x), ex2(a1.y));
-                h0 = __ffma2_rn(a0, h0, __fmul2_rn(su, make_float2(Bk.x, Bk.y)));
-                h1 = __ffma2_rn(a1, h1, __fmul2_rn(su, make_float2(Bk.z, Bk.w)));
-                const float2 C0 = make_float2(Ck.x, Ck.y), C1 = make_float2(Ck.z, Ck.w);
-                const float2 r = __ffma2_rn(C1, h1, __fmul2_rn(C0, h0));
-                yv[k] += r.x + r.y;
-                if constexpr (kSplit) {
-                    p0 = __fmul2_rn(p0, a0);
-                    p1 = __fmul2_rn(p1, a1);
-                    gc[k][0] = __fmul2_rn(C0, p0);
-                    gc[k][1] = __fmul2_rn(C1, p1);
-                }
-            }
-            h = make_float4(h0.x, h0.y, h1.x, h1.y);
-            decay = make_float4(p0.x, p0.y, p1.x, p1.y);
-        }
-        if constexpr (kSplit) {
-            // One barrier per iteration: run w's part is written before it and read behind it, and the
-            // parity keeps a warp that is ahead by one iteration off what others still read.
-            float4* const ex = exchange + (i & 1) * (2 * warps * 32);
-            ex[(2 * warp) * 32 + lane] = h;
-            ex[(2 * warp + 1) * 32 + lane] = decay;
-            __syncthreads();
-            float4 in = carry[((it & 1) * NB + nb) * 32 + lane];
-            for (int w = 0; w < warp; ++w) {
-                const float4 hl = ex[(2 * w) * 32 + lane], pl = ex[(2 * w + 1) * 32 + lane];
-                in.x = fmaf(pl.x, in.x, hl.x);
-                in.y = fmaf(pl.y, in.y, hl.y);
-                in.z = fmaf(pl.z, in.z, hl.z);
-                in.w = fmaf(pl.w, in.w, hl.w);
-            }
-            if (warp == warps - 1)
-                carry[(((it + 1) & 1) * NB + nb) * 32 + lane] =
-                    make_float4(fmaf(decay.x, in.x, h.x), fmaf(decay.y, in.y, h.y), fmaf(decay.z, in.z, h.z),
-                                fmaf(decay.w, in.w, h.w));
+            if (NB > 1) rates(nb);
             if (n > 0) {
-                const float2 i0 = make_float2(in.x, in.y), i1 = make_float2(in.z, in.w);
+                if (nb == 0) {
+                    // once per (token, channel): the step and dt u; past the end both are 0, which
+                    // leaves the state as it is
 #pragma unroll
-                for (int k = 0; k < kTok; ++k) {
-                    const float2 r = __ffma2_rn(gc[k][1], i1, __fmul2_rn(gc[k][0], i0));
-                    yv[k] += r.x + r.y;
+                    for (int q = 0; q < K / SL; ++q) {
+                        const int k = q * SL + j;
+                        float2 v = pair_of(&m.dt[sr][k][2 * cp]);
+                        const float2 u = pair_of(&m.u[sr][k][2 * cp]);
+                        v = __fadd2_rn(v, bias);
+                        if (a.softplus) v = softplus2(v);
+                        v = k < n ? v : both(0.f);
+                        const float2 du = __fmul2_rn(v, u);
+                        m.s[k][cp] = make_float4(v.x, du.x, v.y, du.y);
+                    }
+#pragma unroll
+                    for (int k = 0; k < K; ++k) yv[k] = both(0.f);
+                }
+                if constexpr (sizeof(E) == 2) {
+                    widen<K, NS>(m.Bf, m.B[sb], lane);
+                    widen<K, NS>(m.Cf, m.C[sb], lane);
+                }
+                __syncwarp();
+            }
+            States h, decay;
+            float2 gc[kCut ? K : 1][2][2];               // C_t times the decays up to t
+            decay.fill(1.f);
+            if constexpr (kCut) {
+                h.fill(0.f);
+            } else {
+                // barrier w: the other warp has run its tile, whose states are in carry
+                if (nb == 0 && (it > 0 || warp > 0)) pair_wait<W>(warp);
+                h.load(carry + nb * 64 + lane);
+            }
+            if (n > 0) {
+                const float* Bt;
+                const float* Ct;
+                if constexpr (sizeof(E) == 2) {
+                    Bt = &m.Bf[0][0] + j * 4;
+                    Ct = &m.Cf[0][0] + j * 4;
+                } else {
+                    Bt = &m.B[sb][0][0] + j * 4;
+                    Ct = &m.C[sb][0][0] + j * 4;
+                }
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const float4 s = m.s[k][cp];
+                    const float4 Bk = *reinterpret_cast<const float4*>(Bt + k * NS);
+                    const float4 Ck = *reinterpret_cast<const float4*>(Ct + k * NS);
+                    const float2 Bv[2] = {make_float2(Bk.x, Bk.y), make_float2(Bk.z, Bk.w)};
+                    const float2 Cv[2] = {make_float2(Ck.x, Ck.y), make_float2(Ck.z, Ck.w)};
+                    float part[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float2 st = both(c ? s.z : s.x), du = both(c ? s.w : s.y);
+                        float2 r = both(0.f);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            float2 e = __fmul2_rn(st, A.v[c][i]);
+                            e = make_float2(ex2(e.x), ex2(e.y));
+                            h.v[c][i] = __ffma2_rn(e, h.v[c][i], __fmul2_rn(du, Bv[i]));
+                            r = i ? __ffma2_rn(Cv[i], h.v[c][i], r) : __fmul2_rn(Cv[i], h.v[c][i]);
+                            if constexpr (kCut) {
+                                decay.v[c][i] = k ? __fmul2_rn(decay.v[c][i], e) : e;
+                                gc[k][c][i] = __fmul2_rn(Cv[i], decay.v[c][i]);
+                            }
+                        }
+                        part[c] = r.x + r.y;
+                    }
+                    yv[k] = __fadd2_rn(yv[k], make_float2(part[0], part[1]));
                 }
             }
-        } else {
-            carry[nb * 32 + lane] = h;
-        }
-        if (nb == NB - 1 && n > 0) {
-            // sums over a channel's SL lanes: after the exchanges lane j holds tokens k with k % SL == j
-            float r[kTok / SL];
-            if constexpr (SL == 4) {
-                float half[kTok / 2];
-                const bool up = j & 2, odd = j & 1;
-#pragma unroll
-                for (int q = 0; q < kTok / 2; ++q) {
-                    const int k = (q / 2) * 4 + q % 2;         // tokens with bit 1 clear; k + 2 has it set
-                    const float send = up ? yv[k] : yv[k + 2];
-                    half[q] = (up ? yv[k + 2] : yv[k]) + __shfl_xor_sync(0xffffffffu, send, 2 * CH);
+            if constexpr (kCut) {
+                // The entering state: the first warp's is what the last one left of the round before,
+                // any other's comes from its predecessor (barrier w, and slot w by parity). The first
+                // warp is told once a round. With one state block a predecessor cannot come to its
+                // next hand-over before this one has gone round the chain, and need not wait; with
+                // several, both wait, and the second slot keeps the next hand-over off this one.
+                float4* const slot = slots + (((it * NB + nb) & 1) * W + warp) * 64 + lane;
+                if (warp == 0) {
+                    if (it > 0 && nb == 0) pair_wait<W>(0);
+                } else {
+                    pair_wait<W>(warp);
                 }
+                States in;
+                in.load(warp == 0 ? carry + nb * 64 + lane : slot);
 #pragma unroll
-                for (int q = 0; q < kTok / 4; ++q) {
-                    const float send = odd ? half[2 * q] : half[2 * q + 1];
-                    r[q] = (odd ? half[2 * q + 1] : half[2 * q]) + __shfl_xor_sync(0xffffffffu, send, CH);
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) h.v[c][i] = __ffma2_rn(decay.v[c][i], in.v[c][i], h.v[c][i]);
+                if (warp + 1 < W) {
+                    h.store(slot + 64);
+                    if (NB == 1) pair_arrive<W>(warp + 1);
+                    else pair_wait<W>(warp + 1);
+                } else {
+                    h.store(carry + nb * 64 + lane);
+                    if (nb == NB - 1 && it + 1 < mine) pair_arrive<W>(0);
                 }
-            } else if constexpr (SL == 2) {
-                const bool odd = j & 1;
+                if (n > 0) {
 #pragma unroll
-                for (int q = 0; q < kTok / 2; ++q) {
-                    const float send = odd ? yv[2 * q] : yv[2 * q + 1];
-                    r[q] = (odd ? yv[2 * q + 1] : yv[2 * q]) + __shfl_xor_sync(0xffffffffu, send, CH);
+                    for (int k = 0; k < K; ++k) {
+                        float part[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float2 r =
+                                __ffma2_rn(gc[k][c][1], in.v[c][1], __fmul2_rn(gc[k][c][0], in.v[c][0]));
+                            part[c] = r.x + r.y;
+                        }
+                        yv[k] = __fadd2_rn(yv[k], make_float2(part[0], part[1]));
+                    }
                 }
             } else {
-#pragma unroll
-                for (int q = 0; q < kTok; ++q) r[q] = yv[q];
-            }
-#pragma unroll
-            for (int q = 0; q < kTok / SL; ++q) {
-                const int k = q * SL + j;
-                float v = fmaf(skip, to_float(m.u[sr][k][ch]), r[q]);
-                if (z) v *= silu(to_float(m.z[sr][k][ch]));
-                if (k < n && ch < cols) store_elem(y + (t + k) * a.D + ch, v);
+                h.store(carry + nb * 64 + lane);
+                if (nb == NB - 1 && t + K < t1) pair_arrive<W>(warp ^ 1);
             }
         }
-        nb = nb1;
-        it = it1;
+        if (n <= 0) continue;
+        // sums over the SL lanes of a pair: after the exchanges lane j holds tokens k with k % SL == j
+        float2 r[K / SL];
+        auto give = [&](float2 v, int mask) {
+            return make_float2(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask));
+        };
+        if constexpr (SL == 4) {
+            float2 half[K / 2];
+            const bool up = j & 2, odd = j & 1;
+#pragma unroll
+            for (int q = 0; q < K / 2; ++q) {
+                const int k = (q / 2) * 4 + q % 2;       // bit 1 clear; k + 2 has it set
+                half[q] = __fadd2_rn(up ? yv[k + 2] : yv[k], give(up ? yv[k] : yv[k + 2], 2 * CL));
+            }
+#pragma unroll
+            for (int q = 0; q < K / 4; ++q)
+                r[q] = __fadd2_rn(odd ? half[2 * q + 1] : half[2 * q], give(odd ? half[2 * q] : half[2 * q + 1], CL));
+        } else if constexpr (SL == 2) {
+            const bool odd = j & 1;
+#pragma unroll
+            for (int q = 0; q < K / 2; ++q)
+                r[q] = __fadd2_rn(odd ? yv[2 * q + 1] : yv[2 * q], give(odd ? yv[2 * q] : yv[2 * q + 1], CL));
+        } else {
+#pragma unroll
+            for (int q = 0; q < K; ++q) r[q] = yv[q];
+        }
+        E* to = static_cast<E*>(a.y) + (b * a.T + t + j) * a.D + d0 + 2 * cp;
+#pragma unroll
+        for (int q = 0; q < K / SL; ++q, to += SL * a.D) {
+            const int k = q * SL + j;
+            float2 v = __ffma2_rn(skip, pair_of(&m.u[sr][k][2 * cp]), r[q]);
+            if (zb) {
+                const float2 z = pair_of(&m.z[sr][k][2 * cp]);
+                v = __fmul2_rn(v, make_float2(silu(z.x), silu(z.y)));
+            }
+            if (k < n) {
+                if (p.y_pairs && in1) {
+                    store_pair(to, v);
+                } else {
+                    if (in0) store_elem(to, v.x);
+                    if (in1) store_elem(to + 1, v.y);
+                }
+            }
+        }
     }
     copy_wait<0>();
-    if (!a.fin) return;
-    if constexpr (kSplit) __syncthreads();              // the last warp's carried states
-    if (kSplit && warp != 0) return;
-    if (ch >= cols) return;
-    for (int nb2 = 0; nb2 < NB; ++nb2) {
-        const float4 h = carry[((kSplit ? (ntiles & 1) * NB : 0) + nb2) * 32 + lane];
-        const float v[4] = {h.x, h.y, h.z, h.w};
+    // the warp that wrote the carried states last
+    if (!a.fin || warp != (tiles == 0 ? 0 : kCut ? W - 1 : (tiles - 1) % W)) return;
+    for (int nb = 0; nb < NB; ++nb) {
+        States h;
+        h.load(carry + nb * 64 + lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = nb2 * NS + j * 4 + i;
-            if (n < N) a.fin[state0 + n] = v[i];
+        for (int c = 0; c < 2; ++c) {
+            const float v[4] = {h.v[c][0].x, h.v[c][0].y, h.v[c][1].x, h.v[c][1].y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int n = nb * NS + j * 4 + i;
+                if (n < N && (c ? in1 : in0)) a.fin[(seq * a.D + (c ? db : da)) * N + n] = v[i];
+            }
         }
     }
 }
 
-template <typename E, typename Td, int SL>
-cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
-    constexpr int CH = 32 / SL, NS = 4 * SL;
-    const SelectiveArgs& a = p.a;
-    p.cblocks = (p.per + CH - 1) / CH;
-    p.nblocks = (int)((a.N + NS - 1) / NS);
-    const int64_t units = a.nseq * a.G * p.cblocks;      // warps without a cut
-    const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
-    // Cut the tokens where the channels alone leave the SMs with few warps.
-    int warps = 1;
-    while (warps < kMaxWarps && units * warps < 148 * 12 && len > warps * kTok) warps *= 2;
-    const bool split = warps > 1;
-    if (!split) warps = 4;
-    const int64_t blocks = split ? units : (units + warps - 1) / warps;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t shared = warps * sizeof(WarpMem<E, Td, SL>) +
-                          (split ? (size_t)(4 * warps * 32 + 2 * p.nblocks * 32) : (size_t)warps * p.nblocks * 32) * 16;
-    auto kernel = split ? scan_kernel<E, Td, SL, true> : scan_kernel<E, Td, SL, false>;
+template <typename E, typename Td, int SL, Form F>
+cudaError_t launch_form(const ScanParams& p, int64_t units, cudaStream_t st) {
+    constexpr int W = form_warps(F);
+    const size_t shared = W * sizeof(WarpMem<E, Td, SL, form_tokens(F, SL)>) +
+                          (size_t)(p.nblocks + (F == kAlternate ? 0 : 2 * W)) * 64 * 16;
+    auto kernel = scan_kernel<E, Td, SL, F>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<(unsigned)blocks, warps * 32, shared, st>>>(p);
+    kernel<<<(unsigned)units, W * 32, shared, st>>>(p);
     return cudaGetLastError();
+}
+
+template <typename E, typename Td, int SL>
+cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
+    constexpr int CH = 64 / SL, NS = 4 * SL;
+    const SelectiveArgs& a = p.a;
+    p.cblocks = (p.per + CH - 1) / CH;
+    p.nblocks = (int)((a.N + NS - 1) / NS);
+    const int64_t units = a.nseq * a.G * p.cblocks;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
+    // The cut form where the channels alone leave the SMs with few warps: as many warps a unit as
+    // keep an SM at 16 (a tile's K tokens each, so no more than the sequence fills).
+    constexpr bool kFits16 = 16 * sizeof(WarpMem<E, Td, SL, form_tokens(kCut16, SL)>) <= 160 * 1024;
+    if (units >= 4 * 148 || len <= 32) return launch_form<E, Td, SL, kAlternate>(p, units, st);
+    if (units > 2 * 148 || len <= 64) return launch_form<E, Td, SL, kCut4>(p, units, st);
+    if constexpr (kFits16)
+        if (units <= 148 && len > 128) return launch_form<E, Td, SL, kCut16>(p, units, st);
+    return launch_form<E, Td, SL, kCut8>(p, units, st);
 }
 
 template <typename E, typename Td>
@@ -407,6 +506,7 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
     };
     p.rows16 = p.per % v == 0 && ok(a.u, a.us, v) && ok(a.dt, a.dts, vd) && (!a.z || ok(a.z, a.zs, v));
     p.bc16 = a.N % v == 0 && ok(a.B, a.Bs, v) && ok(a.C, a.Cs, v);
+    p.y_pairs = p.per % 2 == 0 && aligned(a.y, 2 * sizeof(E));
     if (a.N <= 4) return launch_scan<E, Td, 1>(p, st);
     if (a.N <= 8) return launch_scan<E, Td, 2>(p, st);
     return launch_scan<E, Td, 4>(p, st);
