@@ -8,18 +8,29 @@ current stream unless `stream` is given.
 """
 from __future__ import annotations
 
-import ctypes
+import struct
+from typing import NamedTuple
 
 import torch
 
-from ._lib import SSD_BF16, SSD_F32, ConvShapeT, SelectiveShapeT, StridesT, check, lib
+from ._lib import SSD_BF16, SSD_F32, check, lib
 
 _DT = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
-_byref = ctypes.byref
+_F32 = torch.float32
+
+# ssd_conv_shape_t and ssd_selective_shape_t as bytes: building the ctypes structures costs more than
+# the rest of a decoding step's call
+_conv_shape = struct.Struct("=9q2i").pack
+_selective_shape = struct.Struct("=15q4i").pack
 
 
-def _in(t, name, shape, dtype, device, inner=1):
-    """An input: its shape, type and device, and its last `inner` dimensions contiguous."""
+class Strides(NamedTuple):
+    batch: int
+    row: int
+
+
+def _refuse(t, name, shape, dtype, device, inner):
+    """Raises what is wrong with an input."""
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} is required")
     if t.device != device:
@@ -28,22 +39,34 @@ def _in(t, name, shape, dtype, device, inner=1):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
-        step = 1
-        for size, stride in zip(reversed(shape[len(shape) - inner:]),
-                                reversed(t.stride()[len(shape) - inner:])):
-            if size > 1 and stride != step:
-                raise ValueError(f"{name}: the last {inner} dimension(s) must be contiguous")
-            step *= size
-    return t
+    if inner == len(shape):
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name}: the last {inner} dimension(s) must be contiguous")
+
+
+def _inner_contiguous(t, inner):
+    step = 1
+    for size, stride in zip(reversed(t.shape[-inner:]), reversed(t.stride()[-inner:])):
+        if size > 1 and stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _in(t, name, shape, dtype, device, inner=1):
+    """An input: its shape, type and device, and its last `inner` dimensions contiguous."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and (t.is_contiguous() or _inner_contiguous(t, inner))):
+        return t
+    _refuse(t, name, shape, dtype, device, inner)
 
 
 def _whole(t, name, shape, dtype, device):
     """A tensor that has to be contiguous throughout."""
-    _in(t, name, shape, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t
+    _refuse(t, name, shape, dtype, device, len(shape))
 
 
 def _first(t, name, dim):
@@ -59,24 +82,37 @@ def _first(t, name, dim):
 def _strides(t):
     """(batch, row) strides; those of dimensions of one or no element do not matter."""
     s, n = t.stride(), t.shape
-    return StridesT(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+    return Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
 
 
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the raw handle of the device's current stream, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_entries = {}
+
+
 def _call(name, device, stream, *args):
-    fn = getattr(lib(), name)
-    if stream is not None and stream.device != device:
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(lib(), name)
+    if stream is None:
+        handle = _raw_stream(device.index) if _raw_stream is not None else _current_stream(device)
+    elif stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        handle = stream.cuda_stream
     if device.index == torch.cuda.current_device():
-        s = torch.cuda.current_stream() if stream is None else stream
-        st = fn(*args, s.cuda_stream)
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            s = torch.cuda.current_stream() if stream is None else stream
-            st = fn(*args, s.cuda_stream)
+            st = fn(*args, handle)
     if st:
         check(st, name)
 
@@ -99,7 +135,7 @@ def _offsets(cu_seqlens, T, device):
 # ---- the short causal convolution ------------------------------------------
 
 def _conv_args(u, weight, bias, silu, split, out):
-    """Checked shape struct, outputs and whether they go back as a tuple."""
+    """The width, the checked shape as bytes, the outputs and three pointers to them."""
     _first(u, "u", 3)
     b, T, C = u.shape
     dev = u.device
@@ -122,9 +158,8 @@ def _conv_args(u, weight, bias, silu, split, out):
         for i, (y, c) in enumerate(zip(ys, sizes)):
             _whole(y, f"out[{i}]", (b, T, c), u.dtype, dev)
     pad = (0,) * (3 - len(sizes))
-    shape = ConvShapeT(b, T, C, W, (ctypes.c_int64 * 3)(*sizes, *pad), _strides(u), _DT[u.dtype],
-                       1 if silu else 0)
-    return shape, ys, [y.data_ptr() for y in ys] + [None] * len(pad)
+    shape = _conv_shape(b, T, C, W, *sizes, *pad, *_strides(u), _DT[u.dtype], 1 if silu else 0)
+    return W, shape, ys, [y.data_ptr() for y in ys] + [None] * len(pad)
 
 
 def _conv_states(u, W, nseq, initial_states, return_final_states, final_states):
@@ -153,9 +188,9 @@ def ssd_causal_conv1d(u, weight, bias=None, silu: bool = True, split=None, initi
     initial_states, final_states [b, W-1, C] in u's type: the last tokens before and of the
     sequence. Returns y, or (y, final_states).
     """
-    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
-    fin = _conv_states(u, shape.width, shape.batch, initial_states, return_final_states, final_states)
-    _call("ssd_causal_conv1d", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+    W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    fin = _conv_states(u, W, u.shape[0], initial_states, return_final_states, final_states)
+    _call("ssd_causal_conv1d", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), _ptr(initial_states), *yp, _ptr(fin))
     return _conv_result(ys, split, fin, return_final_states)
 
@@ -169,13 +204,13 @@ def ssd_causal_conv1d_varlen(u, weight, bias=None, cu_seqlens=None, silu: bool =
     cu_seqlens: a device int32 tensor [n_docs + 1] (from 0, at most T; rows behind the last
     document are left as they were), or a host list or tensor from 0 to T (copied).
     """
-    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
-    if shape.batch != 1:
+    W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    if u.shape[0] != 1:
         raise ValueError("packed documents need batch 1 (u [1, T, C])")
-    cu = _offsets(cu_seqlens, shape.seqlen, u.device)
+    cu = _offsets(cu_seqlens, u.shape[1], u.device)
     n = cu.numel() - 1
-    fin = _conv_states(u, shape.width, n, initial_states, return_final_states, final_states)
-    _call("ssd_causal_conv1d_varlen", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+    fin = _conv_states(u, W, n, initial_states, return_final_states, final_states)
+    _call("ssd_causal_conv1d_varlen", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), cu.data_ptr(), n, _ptr(initial_states), *yp, _ptr(fin))
     return _conv_result(ys, split, fin, return_final_states)
 
@@ -188,9 +223,9 @@ def ssd_causal_conv1d_step(u, weight, bias, state, silu: bool = True, split=None
         u = u.unsqueeze(1)
         if out is not None:
             out = out.unsqueeze(1) if split is None else [y.unsqueeze(1) for y in out]
-    shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
-    _whole(state, "state", (shape.batch, shape.width - 1, shape.channels), u.dtype, u.device)
-    _call("ssd_causal_conv1d_step", u.device, stream, _byref(shape), u.data_ptr(), weight.data_ptr(),
+    W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
+    _whole(state, "state", (u.shape[0], W - 1, u.shape[2]), u.dtype, u.device)
+    _call("ssd_causal_conv1d_step", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), state.data_ptr(), *yp)
     if one:
         ys = [y.squeeze(1) for y in ys]
@@ -200,7 +235,7 @@ def ssd_causal_conv1d_step(u, weight, bias, state, silu: bool = True, split=None
 # ---- the selective scan ----------------------------------------------------
 
 def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
-    """Checked shape struct, the input pointers in the C order, and y."""
+    """The state size, the checked shape as bytes, the input pointers in the C order, and y."""
     _first(u, "u", 3)
     b, T, Dc = u.shape
     dev, dtype = u.device, u.dtype
@@ -224,11 +259,10 @@ def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
         y = torch.empty((b, T, Dc), dtype=dtype, device=dev)
     else:
         _whole(y, "y", (b, T, Dc), dtype, dev)
-    shape = SelectiveShapeT(b, T, Dc, G, N, _strides(u), _strides(dt),
-                            _strides(z) if z is not None else StridesT(0, 0), _strides(B), _strides(C),
-                            _DT[dtype], _DT[dt.dtype], 1 if dt_softplus else 0, 0)
-    return shape, (u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
-                   _ptr(z), _ptr(dt_bias)), y
+    shape = _selective_shape(b, T, Dc, G, N, *_strides(u), *_strides(dt), *(_strides(z) if z is not None else (0, 0)),
+                             *_strides(B), *_strides(C), _DT[dtype], _DT[dt.dtype], 1 if dt_softplus else 0, 0)
+    return N, shape, (u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
+                      _ptr(z), _ptr(dt_bias)), y
 
 
 def _selective_states(u, nseq, N, initial_states, return_final_states, final_states):
@@ -254,9 +288,9 @@ def ssd_selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     without); A [D, N] fp32, N up to 256; B, C [b, T, G, N]; D, dt_bias [D] fp32 or None;
     z [b, T, D] or None (no gate). States [b, D, N] fp32. Returns y, or (y, final_states).
     """
-    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
-    fin = _selective_states(u, shape.batch, shape.dstate, initial_states, return_final_states, final_states)
-    _call("ssd_selective_scan", u.device, stream, _byref(shape), *ins, _ptr(initial_states), y.data_ptr(),
+    N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    fin = _selective_states(u, u.shape[0], N, initial_states, return_final_states, final_states)
+    _call("ssd_selective_scan", u.device, stream, shape, *ins, _ptr(initial_states), y.data_ptr(),
           _ptr(fin))
     return (y, fin) if return_final_states else y
 
@@ -266,13 +300,13 @@ def ssd_selective_scan_varlen(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_s
                               y=None, final_states=None, stream=None):
     """ssd_selective_scan on a pack of documents (u [1, T, D]) with states [n_docs, D, N];
     cu_seqlens as for ssd_causal_conv1d_varlen."""
-    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
-    if shape.batch != 1:
+    N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    if u.shape[0] != 1:
         raise ValueError("packed documents need batch 1 (u [1, T, D])")
-    cu = _offsets(cu_seqlens, shape.seqlen, u.device)
+    cu = _offsets(cu_seqlens, u.shape[1], u.device)
     n = cu.numel() - 1
-    fin = _selective_states(u, n, shape.dstate, initial_states, return_final_states, final_states)
-    _call("ssd_selective_scan_varlen", u.device, stream, _byref(shape), *ins, cu.data_ptr(), n,
+    fin = _selective_states(u, n, N, initial_states, return_final_states, final_states)
+    _call("ssd_selective_scan_varlen", u.device, stream, shape, *ins, cu.data_ptr(), n,
           _ptr(initial_states), y.data_ptr(), _ptr(fin))
     return (y, fin) if return_final_states else y
 
@@ -286,7 +320,7 @@ def ssd_selective_step(u, dt, A, B, C, D, state, z=None, dt_bias=None, dt_softpl
     one = isinstance(u, torch.Tensor) and u.dim() == 2
     if one:
         u, dt, B, C, z, y = (t.unsqueeze(1) if isinstance(t, torch.Tensor) else t for t in (u, dt, B, C, z, y))
-    shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
-    _whole(state, "state", (shape.batch, shape.channels, shape.dstate), torch.float32, u.device)
-    _call("ssd_selective_step", u.device, stream, _byref(shape), *ins, state.data_ptr(), y.data_ptr())
+    N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
+    _whole(state, "state", (u.shape[0], u.shape[2], N), _F32, u.device)
+    _call("ssd_selective_step", u.device, stream, shape, *ins, state.data_ptr(), y.data_ptr())
     return y.squeeze(1) if one else y

@@ -86,14 +86,15 @@ _SIGS = {
                    + [ctypes.c_size_t, _VP], ctypes.c_int),
     "ssd_gated_rmsnorm": ([ctypes.POINTER(ShapeT), _VP, _VP, _VP, ctypes.c_int64, ctypes.c_float,
                            _VP, _VP], ctypes.c_int),
-    "ssd_causal_conv1d": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 9, ctypes.c_int),
-    "ssd_causal_conv1d_varlen": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 4 + [ctypes.c_int64] + [_VP] * 6,
+    # shapes: a pointer to ConvShapeT or SelectiveShapeT, or their bytes
+    "ssd_causal_conv1d": ([_VP] + [_VP] * 9, ctypes.c_int),
+    "ssd_causal_conv1d_varlen": ([_VP] + [_VP] * 4 + [ctypes.c_int64] + [_VP] * 6,
                                  ctypes.c_int),
-    "ssd_causal_conv1d_step": ([ctypes.POINTER(ConvShapeT)] + [_VP] * 8, ctypes.c_int),
-    "ssd_selective_scan": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 12, ctypes.c_int),
-    "ssd_selective_scan_varlen": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 9 + [ctypes.c_int64]
+    "ssd_causal_conv1d_step": ([_VP] + [_VP] * 8, ctypes.c_int),
+    "ssd_selective_scan": ([_VP] + [_VP] * 12, ctypes.c_int),
+    "ssd_selective_scan_varlen": ([_VP] + [_VP] * 9 + [ctypes.c_int64]
                                   + [_VP] * 4, ctypes.c_int),
-    "ssd_selective_step": ([ctypes.POINTER(SelectiveShapeT)] + [_VP] * 11, ctypes.c_int),
+    "ssd_selective_step": ([_VP] + [_VP] * 11, ctypes.c_int),
     "ssd_chunk_cumsum": ([ctypes.POINTER(ShapeT), _VP, _VP, _VP, _VP], ctypes.c_int),
     "ssd_chunk_state": ([ctypes.POINTER(ShapeT)] + [_VP] * 6, ctypes.c_int),
     "ssd_state_passing": ([ctypes.POINTER(ShapeT)] + [_VP] * 6, ctypes.c_int),

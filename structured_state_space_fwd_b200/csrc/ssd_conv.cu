@@ -38,6 +38,7 @@ struct ConvParams {
     int64_t nseq;
     int run;                     // tokens per warp
     int silu;
+    bool weight16;               // weight starts on 16 bytes
 };
 
 template <typename E, int VW, int W>
@@ -46,9 +47,14 @@ struct Taps {
     __device__ __forceinline__ void load(const ConvParams& p, int64_t c) {
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
+            if (W == 4 && p.weight16) {
+                const float4 q = __ldg(reinterpret_cast<const float4*>(p.weight + (c + i) * W));
+                w[0][i] = q.x; w[1][i] = q.y; w[2 % W][i] = q.z; w[3 % W][i] = q.w;
+            } else {
 #pragma unroll
-            for (int k = 0; k < W; ++k) w[k][i] = p.weight[(c + i) * W + k];
-            bias[i] = p.bias ? p.bias[c + i] : 0.f;
+                for (int k = 0; k < W; ++k) w[k][i] = __ldg(p.weight + (c + i) * W + k);
+            }
+            bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
         }
     }
     // window: the W - 1 tokens before x, oldest first
@@ -237,6 +243,7 @@ ConvParams params_of(const ConvArgs& a, int vw) {
     ConvParams p = {};
     p.u = a.u; p.weight = a.weight; p.bias = a.bias; p.cu = a.cu; p.init = a.init; p.fin = a.final_states;
     p.T = a.T; p.C = a.C; p.ub = a.ub; p.ur = a.ur; p.nseq = a.nseq; p.silu = a.silu;
+    p.weight16 = aligned(a.weight, 16);
     int64_t off = 0;
     for (int i = 0; i < 3; ++i) {
         p.y[i] = a.y[i];

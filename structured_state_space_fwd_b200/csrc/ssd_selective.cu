@@ -513,62 +513,170 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
 }
 
 // ---- decoding --------------------------------------------------------------
-constexpr int kWarps = 4;
-constexpr int kPieces = 8;       // states of a lane: up to 256 over 32 lanes
+//
+// One or a few tokens per sequence from a state in HBM: the state's 8 b D N bytes bound it (at 16
+// states 11 operations and one exponential for each 8 bytes). L lanes share a channel, V states a
+// lane and piece; a thread keeps the pieces of RB batch rows of its channel in registers for all of
+// the call's tokens, so that A (as large as one row's state) is read once for RB rows and RB loads
+// are in flight.
+constexpr int kStepThreads = 128;
 
-// One warp per channel, the states over its lanes.
-template <typename E, typename Td>
-__global__ void __launch_bounds__(kWarps * 32) step_kernel(const SelectiveArgs a) {
-    const int lane = threadIdx.x & 31;
-    const int64_t idx = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    const int64_t b = idx / a.D, d = idx % a.D;
-    if (b >= a.b) return;
-    const int64_t g = d / (a.D / a.G);
-    const int N = (int)a.N;
-    float h[kPieces], A[kPieces];
+struct StepParams {
+    SelectiveArgs a;
+    int64_t cblocks;             // CTAs along the channels
+    int L;                       // lanes of a channel, a power of two up to 32
+    bool bc_wide;                // B and C take loads of V elements
+};
+
+template <int V>
+__device__ __forceinline__ void load_bc(const float* p, bool wide, float (&v)[V]) {
+    if (V == 4 && wide) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        v[0] = q.x; v[1 % V] = q.y; v[2 % V] = q.z; v[3 % V] = q.w;
+    } else {
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-        const int n = lane + 32 * k;
-        A[k] = n < N ? a.A[d * N + n] * kLog2e : 0.f;
-        h[k] = n < N ? a.init[(b * a.D + d) * N + n] : 0.f;
+        for (int i = 0; i < V; ++i) v[i] = p[i];
     }
-    const float D = a.Dskip ? a.Dskip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+}
+template <int V>
+__device__ __forceinline__ void load_bc(const __nv_bfloat16* p, bool wide, float (&v)[V]) {
+    if (V == 4 && wide) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        v[0] = bf16_lo(q.x); v[1 % V] = bf16_hi(q.x); v[2 % V] = bf16_lo(q.y); v[3 % V] = bf16_hi(q.y);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = to_float(p[i]);
+    }
+}
+template <int V>
+__device__ __forceinline__ void load_piece(const float* p, float (&v)[V]) {
+    if constexpr (V == 4) {
+        const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+    } else {
+        v[0] = __ldcs(p);
+    }
+}
+template <int V>
+__device__ __forceinline__ void store_piece(float* p, const float (&v)[V]) {
+    if constexpr (V == 4) {
+        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    } else {
+        __stcs(p, v[0]);
+    }
+}
+
+template <typename E, typename Td, int V, int KP, int RB>
+__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams p) {
+    const SelectiveArgs& a = p.a;
+    const int L = p.L, j = threadIdx.x & (L - 1), N = (int)a.N;
+    const int64_t d = blockIdx.x % p.cblocks * (kStepThreads / L) + threadIdx.x / L;
+    const int64_t b0 = blockIdx.x / p.cblocks * RB;
+    const bool live = d < a.D;                           // whole groups of L lanes
+    const int64_t dc = live ? d : 0, g = dc / (a.D / a.G);
+    const int rows = live ? (int)min(a.b - b0, (int64_t)RB) : 0;
+    float h[RB][KP][V], A[KP][V];
+    float* const state = a.fin + (b0 * a.D + dc) * N;
+#pragma unroll
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int k = 0; k < KP; ++k) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[r][k][i] = 0.f;
+            if (r < rows && (j + k * L) * V < N) load_piece<V>(state + r * a.D * N + (j + k * L) * V, h[r][k]);
+        }
+#pragma unroll
+    for (int k = 0; k < KP; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            A[k][i] = (j + k * L) * V < N ? a.A[dc * N + (j + k * L) * V + i] * kLog2e : 0.f;
+    const float skip = a.Dskip ? a.Dskip[dc] : 0.f, bias = a.dt_bias ? a.dt_bias[dc] : 0.f;
     for (int64_t t = 0; t < a.T; ++t) {
-        const float u = to_float(static_cast<const E*>(a.u)[b * a.us.batch + t * a.us.row + d]);
-        float dt = to_float(static_cast<const Td*>(a.dt)[b * a.dts.batch + t * a.dts.row + d]) + bias;
-        if (a.softplus) dt = softplus(dt);
-        const E* B = static_cast<const E*>(a.B) + b * a.Bs.batch + t * a.Bs.row + g * N;
-        const E* C = static_cast<const E*>(a.C) + b * a.Cs.batch + t * a.Cs.row + g * N;
-        float y = 0.f;
+        float dt[RB], u[RB], z[RB], y[RB];
 #pragma unroll
-        for (int k = 0; k < kPieces; ++k) {
-            const int n = lane + 32 * k;
-            if (n < N) {
-                h[k] = fmaf(ex2(dt * A[k]), h[k], dt * u * to_float(B[n]));
-                y = fmaf(to_float(C[n]), h[k], y);
-            }
+        for (int r = 0; r < RB; ++r) {
+            const int64_t b = b0 + (r < rows ? r : 0);
+            dt[r] = to_float(static_cast<const Td*>(a.dt)[b * a.dts.batch + t * a.dts.row + dc]) + bias;
+            u[r] = to_float(static_cast<const E*>(a.u)[b * a.us.batch + t * a.us.row + dc]);
+            z[r] = a.z ? to_float(static_cast<const E*>(a.z)[b * a.zs.batch + t * a.zs.row + dc]) : 0.f;
         }
-        for (int off = 16; off > 0; off >>= 1) y += __shfl_xor_sync(0xffffffffu, y, off);
-        if (lane == 0) {
-            y = fmaf(D, u, y);
-            if (a.z) y *= silu(to_float(static_cast<const E*>(a.z)[b * a.zs.batch + t * a.zs.row + d]));
-            store_elem(static_cast<E*>(a.y) + (b * a.T + t) * a.D + d, y);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            const int64_t b = b0 + (r < rows ? r : 0);
+            const E* B = static_cast<const E*>(a.B) + b * a.Bs.batch + t * a.Bs.row + g * N;
+            const E* C = static_cast<const E*>(a.C) + b * a.Cs.batch + t * a.Cs.row + g * N;
+            if (a.softplus) dt[r] = softplus(dt[r]);
+            const float du = dt[r] * u[r];
+            float acc = 0.f;
+#pragma unroll
+            for (int k = 0; k < KP; ++k)
+                if ((j + k * L) * V < N) {
+                    float Bv[V], Cv[V];
+                    load_bc<V>(B + (j + k * L) * V, p.bc_wide, Bv);
+                    load_bc<V>(C + (j + k * L) * V, p.bc_wide, Cv);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        h[r][k][i] = fmaf(ex2(dt[r] * A[k][i]), h[r][k][i], du * Bv[i]);
+                        acc = fmaf(Cv[i], h[r][k][i], acc);
+                    }
+                }
+            y[r] = acc;
+        }
+        for (int off = L >> 1; off > 0; off >>= 1)
+#pragma unroll
+            for (int r = 0; r < RB; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+            // lane r % L writes row r
+            if (j != r % L || r >= rows) continue;
+            float v = fmaf(skip, u[r], y[r]);
+            if (a.z) v *= silu(z[r]);
+            store_elem(static_cast<E*>(a.y) + ((b0 + r) * a.T + t) * a.D + dc, v);
         }
     }
 #pragma unroll
-    for (int k = 0; k < kPieces; ++k) {
-        const int n = lane + 32 * k;
-        if (n < N) a.fin[(b * a.D + d) * N + n] = h[k];
-    }
+    for (int r = 0; r < RB; ++r)
+#pragma unroll
+        for (int k = 0; k < KP; ++k)
+            if (r < rows && (j + k * L) * V < N) store_piece<V>(state + r * a.D * N + (j + k * L) * V, h[r][k]);
+}
+
+template <typename E, typename Td, int V, int KP>
+cudaError_t launch_step(StepParams p, cudaStream_t st) {
+    const SelectiveArgs& a = p.a;
+    const int per_cta = kStepThreads / p.L;
+    p.cblocks = (a.D + per_cta - 1) / per_cta;
+    // Four batch rows a thread once that leaves every SM some CTAs; fewer rows finish sooner one each.
+    constexpr int RB = KP <= 4 ? 4 : 2;
+    const bool many = p.cblocks * ((a.b + RB - 1) / RB) >= 2 * 148;
+    const int64_t blocks = p.cblocks * (many ? (a.b + RB - 1) / RB : a.b);
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (many)
+        step_kernel<E, Td, V, KP, RB><<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
+    else
+        step_kernel<E, Td, V, KP, 1><<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename E, typename Td>
 cudaError_t step_any(const SelectiveArgs& a, cudaStream_t st) {
-    const int64_t blocks = (a.nseq * a.D + kWarps - 1) / kWarps;
-    if (blocks == 0 || a.T == 0) return cudaSuccess;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    step_kernel<E, Td><<<(unsigned)blocks, kWarps * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.b == 0 || a.T == 0) return cudaSuccess;
+    StepParams p = {};
+    p.a = a;
+    const bool wide = a.N % 4 == 0 && aligned(a.fin, 16);
+    const int64_t pieces = wide ? a.N / 4 : a.N;
+    p.L = 1;
+    while (p.L < 32 && p.L < pieces) p.L *= 2;
+    auto ok = [](const void* q, const ssd_strides_t& s) {
+        return aligned(q, 4 * sizeof(E)) && s.batch % 4 == 0 && s.row % 4 == 0;
+    };
+    p.bc_wide = ok(a.B, a.Bs) && ok(a.C, a.Cs);
+    const int64_t kp = (pieces + p.L - 1) / p.L;
+    if (wide) return kp == 1 ? launch_step<E, Td, 4, 1>(p, st) : launch_step<E, Td, 4, 2>(p, st);
+    if (kp == 1) return launch_step<E, Td, 1, 1>(p, st);
+    if (kp == 2) return launch_step<E, Td, 1, 2>(p, st);
+    if (kp <= 4) return launch_step<E, Td, 1, 4>(p, st);
+    return launch_step<E, Td, 1, 8>(p, st);
 }
 
 }  // namespace
