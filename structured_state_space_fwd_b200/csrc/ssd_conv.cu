@@ -20,7 +20,7 @@ namespace ssd {
 namespace {
 
 constexpr int kRunWarps = 8;     // token runs per CTA: one per warp, on the same 32 channel vectors
-constexpr int kBatch = 4;        // tokens whose loads a thread issues together
+constexpr int kBatch = 8;        // tokens whose loads a thread issues together
 
 struct ConvParams {
     const void* u;
@@ -41,43 +41,106 @@ struct ConvParams {
     bool weight16;               // weight starts on 16 bytes
 };
 
-template <typename E, int VW, int W>
+// A thread's VW channels as packed pairs (VW = 1: one value).
+template <int VW>
+struct Lanes {
+    using T = float2;
+    static constexpr int M = VW / 2;
+};
+template <>
+struct Lanes<1> {
+    using T = float;
+    static constexpr int M = 1;
+};
+template <int VW>
+struct Vec {
+    using T = typename Lanes<VW>::T;
+    static constexpr int M = Lanes<VW>::M;
+    T v[M];
+};
+__device__ __forceinline__ Vec<4> widen(uint2 q) {        // 4 bf16
+    return {{make_float2(bf16_lo(q.x), bf16_hi(q.x)), make_float2(bf16_lo(q.y), bf16_hi(q.y))}};
+}
+__device__ __forceinline__ Vec<4> widen(float4 q) { return {{make_float2(q.x, q.y), make_float2(q.z, q.w)}}; }
+__device__ __forceinline__ Vec<1> widen(float q) { return {{q}}; }
+__device__ __forceinline__ Vec<1> widen(__nv_bfloat16 q) { return {{__bfloat162float(q)}}; }
+__device__ __forceinline__ void narrow(const Vec<4>& v, uint2& q) {
+    q = make_uint2(pack_bf16(v.v[0].x, v.v[0].y), pack_bf16(v.v[1].x, v.v[1].y));
+}
+__device__ __forceinline__ void narrow(const Vec<4>& v, float4& q) {
+    q = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+}
+__device__ __forceinline__ void narrow(const Vec<1>& v, float& q) { q = v.v[0]; }
+__device__ __forceinline__ void narrow(const Vec<1>& v, __nv_bfloat16& q) { q = __float2bfloat16_rn(v.v[0]); }
+// VW elements as they lie in memory
+template <typename E, int VW>
+struct Pack {
+    using T = E;
+};
+template <>
+struct Pack<float, 4> {
+    using T = float4;
+};
+template <>
+struct Pack<__nv_bfloat16, 4> {
+    using T = uint2;
+};
+template <typename P>
+__device__ __forceinline__ P zero_pack() {
+    if constexpr (sizeof(P) == 16) return make_float4(0.f, 0.f, 0.f, 0.f);
+    else if constexpr (sizeof(P) == 8) return make_uint2(0, 0);
+    else return P(0.f);
+}
+
+template <int VW, int W>
 struct Taps {
-    float w[W][VW], bias[VW];
+    Vec<VW> w[W], bias;
     __device__ __forceinline__ void load(const ConvParams& p, int64_t c) {
+        float f[VW][W], b[VW];
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
             if (W == 4 && p.weight16) {
                 const float4 q = __ldg(reinterpret_cast<const float4*>(p.weight + (c + i) * W));
-                w[0][i] = q.x; w[1][i] = q.y; w[2 % W][i] = q.z; w[3 % W][i] = q.w;
+                f[i][0] = q.x; f[i][1] = q.y; f[i][2 % W] = q.z; f[i][3 % W] = q.w;
             } else {
 #pragma unroll
-                for (int k = 0; k < W; ++k) w[k][i] = __ldg(p.weight + (c + i) * W + k);
+                for (int k = 0; k < W; ++k) f[i][k] = __ldg(p.weight + (c + i) * W + k);
             }
-            bias[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
+            b[i] = p.bias ? __ldg(p.bias + c + i) : 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < Vec<VW>::M; ++m) {
+            if constexpr (VW == 1) {
+#pragma unroll
+                for (int k = 0; k < W; ++k) w[k].v[0] = f[0][k];
+                bias.v[0] = b[0];
+            } else {
+#pragma unroll
+                for (int k = 0; k < W; ++k) w[k].v[m] = make_float2(f[2 * m][k], f[2 * m + 1][k]);
+                bias.v[m] = make_float2(b[2 * m], b[2 * m + 1]);
+            }
         }
     }
     // window: the W - 1 tokens before x, oldest first
-    __device__ __forceinline__ void apply(const float (&window)[W - 1][VW], const float (&x)[VW], int act,
-                                          float (&y)[VW]) const {
+    template <bool kSilu>
+    __device__ __forceinline__ Vec<VW> apply(const Vec<VW> (&window)[W - 1], const Vec<VW>& x) const {
+        Vec<VW> y;
 #pragma unroll
-        for (int i = 0; i < VW; ++i) {
-            float v = bias[i];
+        for (int m = 0; m < Vec<VW>::M; ++m) {
+            typename Vec<VW>::T v = bias.v[m];
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) v = fmaf(w[k][i], window[k][i], v);
-            v = fmaf(w[W - 1][i], x[i], v);
-            y[i] = act ? silu(v) : v;
+            for (int k = 0; k < W - 1; ++k) v = fma_(w[k].v[m], window[k].v[m], v);
+            v = fma_(w[W - 1].v[m], x.v[m], v);
+            y.v[m] = kSilu ? silu(v) : v;
         }
+        return y;
     }
 };
 template <int W, int VW>
-__device__ __forceinline__ void push(float (&window)[W - 1][VW], const float (&x)[VW]) {
+__device__ __forceinline__ void push(Vec<VW> (&window)[W - 1], const Vec<VW>& x) {
 #pragma unroll
-    for (int i = 0; i < VW; ++i) {
-#pragma unroll
-        for (int k = 0; k + 1 < W - 1; ++k) window[k][i] = window[k + 1][i];
-        window[W - 2][i] = x[i];
-    }
+    for (int k = 0; k + 1 < W - 1; ++k) window[k] = window[k + 1];
+    window[W - 2] = x;
 }
 
 // Where channel c of batch row b goes: its output's first token, and the stride of its tokens.
@@ -104,7 +167,7 @@ __device__ __forceinline__ int64_t find_doc(const int* cu, int64_t n, int64_t t)
     return lo;
 }
 
-template <typename E, int VW, int W, bool kPacked>
+template <typename E, int VW, int W, bool kPacked, bool kSilu>
 __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p) {
     using Raw = typename Pack<E, VW>::T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -145,7 +208,7 @@ __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p
     const int64_t c = vec * VW;
     const E* u = static_cast<const E*>(p.u) + b * p.ub + c;
     const Out<E> out(p, b, c);
-    Taps<E, VW, W> taps;
+    Taps<VW, W> taps;
     taps.load(p, c);
 
     int64_t seq = b, start = 0, next = limit;                // the sequence and where it starts and ends
@@ -155,7 +218,7 @@ __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p
         start = start < 0 ? 0 : (start > t0 ? t0 : start);
         next = p.cu[seq + 1];
     }
-    float window[W - 1][VW];
+    Vec<VW> window[W - 1];
     auto open = [&](int64_t t) {                             // the W - 1 tokens before t
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
@@ -165,36 +228,38 @@ __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p
                 r = *reinterpret_cast<const Raw*>(u + s * p.ur);
             else if (init && s - start + (W - 1) >= 0)
                 r = *reinterpret_cast<const Raw*>(init + (seq * (W - 1) + s - start + (W - 1)) * p.C + c);
-            unpack(r, window[k]);
+            window[k] = widen(r);
         }
     };
     open(t0);
-    for (int64_t t = t0; t < t1; t += kBatch) {
+    auto one = [&](int64_t t, const Raw& raw) {
+        const Vec<VW> x = widen(raw);
+        Raw o;
+        narrow(taps.template apply<kSilu>(window, x), o);
+        push<W>(window, x);
+        __stcs(reinterpret_cast<Raw*>(out.y + t * out.stride), o);
+    };
+    int64_t t = t0;
+    for (; t + kBatch <= t1; t += kBatch) {
         Raw raw[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-            if (t + i < t1) raw[i] = __ldcs(reinterpret_cast<const Raw*>(u + (t + i) * p.ur));
+        for (int i = 0; i < kBatch; ++i) raw[i] = __ldcs(reinterpret_cast<const Raw*>(u + (t + i) * p.ur));
+        if (kPacked && t + kBatch > next) break;             // a document starts among these
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (t + i >= t1) break;
-            if constexpr (kPacked) {
-                if (t + i >= next && seq + 1 < p.nseq) {     // a document starts here: the last that does
-                    do {
-                        ++seq;
-                        next = p.cu[seq + 1];
-                    } while (t + i >= next && seq + 1 < p.nseq);
-                    start = t + i;
-                    open(t + i);
-                }
+        for (int i = 0; i < kBatch; ++i) one(t + i, raw[i]);
+    }
+    for (; t < t1; ++t) {
+        if constexpr (kPacked) {
+            if (t >= next && seq + 1 < p.nseq) {             // a document starts here: the last that does
+                do {
+                    ++seq;
+                    next = p.cu[seq + 1];
+                } while (t >= next && seq + 1 < p.nseq);
+                start = t;
+                open(t);
             }
-            float x[VW], v[VW];
-            unpack(raw[i], x);
-            taps.apply(window, x, p.silu, v);
-            push<W>(window, x);
-            Raw o;
-            pack(v, o);
-            __stcs(reinterpret_cast<Raw*>(out.y + (t + i) * out.stride), o);
         }
+        one(t, *reinterpret_cast<const Raw*>(u + t * p.ur));
     }
 }
 
@@ -208,34 +273,33 @@ __global__ void __launch_bounds__(128) conv_step_kernel(const ConvParams p, E* s
     E* st = state + b * (W - 1) * p.C + c;
     const E* u = static_cast<const E*>(p.u) + b * p.ub + c;
     const Out<E> out(p, b, c);
-    float window[W - 1][VW];
+    Vec<VW> window[W - 1];
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) unpack(*reinterpret_cast<const Raw*>(st + k * p.C), window[k]);
-    Taps<E, VW, W> taps;
+    for (int k = 0; k < W - 1; ++k) window[k] = widen(*reinterpret_cast<const Raw*>(st + k * p.C));
+    Taps<VW, W> taps;
     taps.load(p, c);
     for (int64_t t = 0; t < p.T; ++t) {
-        float x[VW], v[VW];
-        unpack(*reinterpret_cast<const Raw*>(u + t * p.ur), x);
-        taps.apply(window, x, p.silu, v);
-        push<W>(window, x);
+        const Vec<VW> x = widen(*reinterpret_cast<const Raw*>(u + t * p.ur));
         Raw o;
-        pack(v, o);
+        narrow(p.silu ? taps.template apply<true>(window, x) : taps.template apply<false>(window, x), o);
+        push<W>(window, x);
         *reinterpret_cast<Raw*>(out.y + t * out.stride) = o;
     }
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
         Raw o;
-        pack(window[k], o);
+        narrow(window[k], o);
         *reinterpret_cast<Raw*>(st + k * p.C) = o;
     }
 }
 
+// Whether the tensors take accesses of 4 channels (8 bytes of bf16, 16 of fp32).
 bool wide(const ConvArgs& a, const void* state) {
-    const int es = a.dtype == SSD_BF16 ? 2 : 4, vw = 16 / es;
+    const int es = a.dtype == SSD_BF16 ? 2 : 4, vw = 4;
     if (a.C % vw || a.ub % vw || a.ur % vw || a.oc[0] % vw || a.oc[1] % vw || a.oc[2] % vw) return false;
     for (const void* q : {a.u, (const void*)a.y[0], (const void*)a.y[1], (const void*)a.y[2], a.init,
                           (const void*)a.final_states, state})
-        if (!aligned(q, 16)) return false;
+        if (!aligned(q, 4 * es)) return false;
     return true;
 }
 
@@ -264,7 +328,7 @@ cudaError_t conv_w(const ConvArgs& a, cudaStream_t st) {
     ConvParams p = params_of(a, VW);
     // Runs of 64 tokens read 5 % more rows than they write (L2 holds the halo); shorter ones where
     // there would be too few warps to keep the memory busy.
-    int run = 64;
+    int run = 32;
     while (run > kBatch && p.nvg * a.b * ((a.T + run - 1) / run) < 148 * 24) run /= 2;
     p.run = run;
     p.run_blocks = (a.T + (int64_t)run * kRunWarps - 1) / ((int64_t)run * kRunWarps);
@@ -273,10 +337,9 @@ cudaError_t conv_w(const ConvArgs& a, cudaStream_t st) {
     const int64_t blocks = p.main_blocks + fin_blocks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (a.cu)
-        conv_kernel<E, VW, W, true><<<(unsigned)blocks, kRunWarps * 32, 0, st>>>(p);
-    else
-        conv_kernel<E, VW, W, false><<<(unsigned)blocks, kRunWarps * 32, 0, st>>>(p);
+    auto kernel = a.cu ? (a.silu ? conv_kernel<E, VW, W, true, true> : conv_kernel<E, VW, W, true, false>)
+                       : (a.silu ? conv_kernel<E, VW, W, false, true> : conv_kernel<E, VW, W, false, false>);
+    kernel<<<(unsigned)blocks, kRunWarps * 32, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -302,7 +365,7 @@ cudaError_t conv_v(const ConvArgs& a, void* state, bool step, cudaStream_t st) {
 cudaError_t conv_any(const ConvArgs& a, void* state, bool step, cudaStream_t st) {
     const bool v = wide(a, state);
     if (a.dtype == SSD_BF16)
-        return v ? conv_v<__nv_bfloat16, 8>(a, state, step, st) : conv_v<__nv_bfloat16, 1>(a, state, step, st);
+        return v ? conv_v<__nv_bfloat16, 4>(a, state, step, st) : conv_v<__nv_bfloat16, 1>(a, state, step, st);
     return v ? conv_v<float, 4>(a, state, step, st) : conv_v<float, 1>(a, state, step, st);
 }
 

@@ -139,8 +139,6 @@ __device__ __forceinline__ void store_pair(float* p, float2 v) { *reinterpret_ca
 __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
 }
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 template <int K, int NS>
 __device__ __forceinline__ void widen(float (*dst)[NS], const __nv_bfloat16 (*src)[NS], int lane) {
 #pragma unroll
@@ -292,7 +290,7 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
                         float2 v = pair_of(&m.dt[sr][k][2 * cp]);
                         const float2 u = pair_of(&m.u[sr][k][2 * cp]);
                         v = __fadd2_rn(v, bias);
-                        if (a.softplus) v = softplus2(v);
+                        if (a.softplus) v = softplus(v);
                         v = k < n ? v : both(0.f);
                         const float2 du = __fmul2_rn(v, u);
                         m.s[k][cp] = make_float4(v.x, du.x, v.y, du.y);
@@ -341,7 +339,7 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             float2 e = __fmul2_rn(st, A.v[c][i]);
-                            e = make_float2(ex2(e.x), ex2(e.y));
+                            e = ex2(e);
                             h.v[c][i] = __ffma2_rn(e, h.v[c][i], __fmul2_rn(du, Bv[i]));
                             r = i ? __ffma2_rn(Cv[i], h.v[c][i], r) : __fmul2_rn(Cv[i], h.v[c][i]);
                             if constexpr (kCut) {
@@ -431,7 +429,7 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
             float2 v = __ffma2_rn(skip, pair_of(&m.u[sr][k][2 * cp]), r[q]);
             if (zb) {
                 const float2 z = pair_of(&m.z[sr][k][2 * cp]);
-                v = __fmul2_rn(v, make_float2(silu(z.x), silu(z.y)));
+                v = __fmul2_rn(v, silu(z));
             }
             if (k < n) {
                 if (p.y_pairs && in1) {
@@ -514,18 +512,19 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
 
 // ---- decoding --------------------------------------------------------------
 //
-// One or a few tokens per sequence from a state in HBM: the state's 8 b D N bytes bound it (at 16
-// states 11 operations and one exponential for each 8 bytes). L lanes share a channel, V states a
-// lane and piece; a thread keeps the pieces of RB batch rows of its channel in registers for all of
-// the call's tokens, so that A (as large as one row's state) is read once for RB rows and RB loads
-// are in flight.
+// One or a few tokens per sequence from a state in HBM: the state's 8 b D N bytes bound it. L lanes
+// share a channel, V states a lane and piece; a thread keeps the pieces of kRows batch rows of its
+// channel in registers for all of the call's tokens, so that A (as large as one row's state) is read
+// once for them and their loads are in flight together. What a (row, channel) needs once - the step,
+// dt u, the gate - is computed by one of the L lanes and handed to the others; the rows' sums are
+// exchanged so that each row ends in the lane that holds its u and gate.
 constexpr int kStepThreads = 128;
 
 struct StepParams {
     SelectiveArgs a;
     int64_t cblocks;             // CTAs along the channels
     int L;                       // lanes of a channel, a power of two up to 32
-    bool bc_wide;                // B and C take loads of V elements
+    bool a_wide, bc_wide;        // A (B and C) take loads of V elements
 };
 
 template <int V>
@@ -566,79 +565,139 @@ __device__ __forceinline__ void store_piece(float* p, const float (&v)[V]) {
     }
 }
 
-template <typename E, typename Td, int V, int KP, int RB>
+// R rows a thread, Q = R / (lanes that prepare them): a lane prepares rows q (R / Q) + j, q < Q.
+template <typename E, typename Td, int V, int KP, int R, int Q>
 __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams p) {
+    constexpr int PL = R / Q;                            // lanes that prepare rows, at most L
     const SelectiveArgs& a = p.a;
     const int L = p.L, j = threadIdx.x & (L - 1), N = (int)a.N;
     const int64_t d = blockIdx.x % p.cblocks * (kStepThreads / L) + threadIdx.x / L;
-    const int64_t b0 = blockIdx.x / p.cblocks * RB;
+    const int64_t b0 = blockIdx.x / p.cblocks * R;
     const bool live = d < a.D;                           // whole groups of L lanes
     const int64_t dc = live ? d : 0, g = dc / (a.D / a.G);
-    const int rows = live ? (int)min(a.b - b0, (int64_t)RB) : 0;
-    float h[RB][KP][V], A[KP][V];
-    float* const state = a.fin + (b0 * a.D + dc) * N;
+    const int rows = live ? (int)min(a.b - b0, (int64_t)R) : 0;
+    float h[R][KP][V], A[KP][V];
+    float* const state = a.fin + (b0 * a.D + dc) * N + j * V;
+    const int64_t next_row = a.D * N;
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < KP; ++k) {
 #pragma unroll
             for (int i = 0; i < V; ++i) h[r][k][i] = 0.f;
-            if (r < rows && (j + k * L) * V < N) load_piece<V>(state + r * a.D * N + (j + k * L) * V, h[r][k]);
+            if (r < rows && (j + k * L) * V < N) load_piece<V>(state + r * next_row + k * L * V, h[r][k]);
         }
+    // the rows this lane prepares (j % PL: with more lanes than rows the others repeat them)
+    const int own = j % PL;
+    const Td* dtp[Q];
+    const E* up[Q];
+    const E* zp[Q];
 #pragma unroll
-    for (int k = 0; k < KP; ++k)
+    for (int q = 0; q < Q; ++q) {
+        const int64_t b = b0 + (q * PL + own < rows ? q * PL + own : 0);
+        dtp[q] = static_cast<const Td*>(a.dt) + b * a.dts.batch + dc;
+        up[q] = static_cast<const E*>(a.u) + b * a.us.batch + dc;
+        zp[q] = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + dc : nullptr;
+    }
+    const E* Bp = static_cast<const E*>(a.B) + b0 * a.Bs.batch + g * N + j * V;
+    const E* Cp = static_cast<const E*>(a.C) + b0 * a.Cs.batch + g * N + j * V;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            A[k][i] = (j + k * L) * V < N ? a.A[dc * N + (j + k * L) * V + i] * kLog2e : 0.f;
+    for (int k = 0; k < KP; ++k) {
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+        if ((j + k * L) * V < N) load_bc<V>(a.A + dc * N + (j + k * L) * V, p.a_wide, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) A[k][i] = v[i] * kLog2e;
+    }
     const float skip = a.Dskip ? a.Dskip[dc] : 0.f, bias = a.dt_bias ? a.dt_bias[dc] : 0.f;
+    E* y = static_cast<E*>(a.y) + (b0 + own) * a.T * a.D + dc;
     for (int64_t t = 0; t < a.T; ++t) {
-        float dt[RB], u[RB], z[RB], y[RB];
+        float dt[Q], u[Q], z[Q], acc[R];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const int64_t b = b0 + (r < rows ? r : 0);
-            dt[r] = to_float(static_cast<const Td*>(a.dt)[b * a.dts.batch + t * a.dts.row + dc]) + bias;
-            u[r] = to_float(static_cast<const E*>(a.u)[b * a.us.batch + t * a.us.row + dc]);
-            z[r] = a.z ? to_float(static_cast<const E*>(a.z)[b * a.zs.batch + t * a.zs.row + dc]) : 0.f;
+        for (int q = 0; q < Q; ++q) {
+            dt[q] = to_float(dtp[q][t * a.dts.row]);
+            u[q] = to_float(up[q][t * a.us.row]);
+            z[q] = a.z ? to_float(zp[q][t * a.zs.row]) : 0.f;
+        }
+        // all of B and C before the first use
+        float Bv[R][KP][V], Cv[R][KP][V];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < KP; ++k) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) Bv[r][k][i] = Cv[r][k][i] = 0.f;
+                if (r < rows && (j + k * L) * V < N) {
+                    load_bc<V>(Bp + r * a.Bs.batch + t * a.Bs.row + k * L * V, p.bc_wide, Bv[r][k]);
+                    load_bc<V>(Cp + r * a.Cs.batch + t * a.Cs.row + k * L * V, p.bc_wide, Cv[r][k]);
+                }
+            }
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            dt[q] += bias;
+            if (a.softplus) dt[q] = softplus(dt[q]);
         }
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            const int64_t b = b0 + (r < rows ? r : 0);
-            const E* B = static_cast<const E*>(a.B) + b * a.Bs.batch + t * a.Bs.row + g * N;
-            const E* C = static_cast<const E*>(a.C) + b * a.Cs.batch + t * a.Cs.row + g * N;
-            if (a.softplus) dt[r] = softplus(dt[r]);
-            const float du = dt[r] * u[r];
-            float acc = 0.f;
+        for (int r = 0; r < R; ++r) {
+            const float dtr = __shfl_sync(0xffffffffu, dt[r / PL], r % PL, L);
+            const float du = dtr * __shfl_sync(0xffffffffu, u[r / PL], r % PL, L);
+            acc[r] = 0.f;
 #pragma unroll
             for (int k = 0; k < KP; ++k)
-                if ((j + k * L) * V < N) {
-                    float Bv[V], Cv[V];
-                    load_bc<V>(B + (j + k * L) * V, p.bc_wide, Bv);
-                    load_bc<V>(C + (j + k * L) * V, p.bc_wide, Cv);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        h[r][k][i] = fmaf(ex2(dt[r] * A[k][i]), h[r][k][i], du * Bv[i]);
-                        acc = fmaf(Cv[i], h[r][k][i], acc);
-                    }
+                for (int i = 0; i < V; ++i) {
+                    h[r][k][i] = fmaf(ex2(dtr * A[k][i]), h[r][k][i], du * Bv[r][k][i]);
+                    acc[r] = fmaf(Cv[r][k][i], h[r][k][i], acc[r]);
                 }
-            y[r] = acc;
         }
-        for (int off = L >> 1; off > 0; off >>= 1)
+        // lane j ends with the sums of the rows q PL + j % PL
+        float sum[Q];
+        if constexpr (PL == 4) {
+            const bool up2 = j & 2, odd = j & 1;
+            const float lo = (up2 ? acc[2] : acc[0]) + __shfl_xor_sync(0xffffffffu, up2 ? acc[0] : acc[2], 2);
+            const float hi = (up2 ? acc[3] : acc[1]) + __shfl_xor_sync(0xffffffffu, up2 ? acc[1] : acc[3], 2);
+            sum[0] = (odd ? hi : lo) + __shfl_xor_sync(0xffffffffu, odd ? lo : hi, 1);
+        } else if constexpr (PL == 2) {
+            const bool odd = j & 1;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) y[r] += __shfl_xor_sync(0xffffffffu, y[r], off);
+            for (int q = 0; q < Q; ++q)
+                sum[q] = (odd ? acc[2 * q + 1] : acc[2 * q]) +
+                         __shfl_xor_sync(0xffffffffu, odd ? acc[2 * q] : acc[2 * q + 1], 1);
+        } else {
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-            // lane r % L writes row r
-            if (j != r % L || r >= rows) continue;
-            float v = fmaf(skip, u[r], y[r]);
-            if (a.z) v *= silu(z[r]);
-            store_elem(static_cast<E*>(a.y) + ((b0 + r) * a.T + t) * a.D + dc, v);
+            for (int q = 0; q < Q; ++q) sum[q] = acc[q];
         }
+        for (int off = PL; off < L; off <<= 1)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], off);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+            if (j < PL && q * PL + own < rows) {
+                float v = fmaf(skip, u[q], sum[q]);
+                if (a.z) v *= silu(z[q]);
+                store_elem(y + (q * PL * a.T + t) * a.D, v);
+            }
     }
 #pragma unroll
-    for (int r = 0; r < RB; ++r)
+    for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int k = 0; k < KP; ++k)
-            if (r < rows && (j + k * L) * V < N) store_piece<V>(state + r * a.D * N + (j + k * L) * V, h[r][k]);
+            if (r < rows && (j + k * L) * V < N) store_piece<V>(state + r * next_row + k * L * V, h[r][k]);
+}
+
+template <typename E, typename Td, int V, int KP, int R>
+cudaError_t launch_rows(const StepParams& p, int64_t blocks, cudaStream_t st) {
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    // as many lanes prepare rows as there are, of the L lanes (32 with more than one piece)
+    constexpr int kMost = R < 4 ? R : 4;
+    auto kernel = step_kernel<E, Td, V, KP, R, R / kMost>;
+    if constexpr (KP == 1 && R > 1) {
+        if (p.L == 1) kernel = step_kernel<E, Td, V, KP, R, R>;
+        if (p.L == 2) kernel = step_kernel<E, Td, V, KP, R, R / 2>;
+    }
+    kernel<<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 template <typename E, typename Td, int V, int KP>
@@ -646,16 +705,11 @@ cudaError_t launch_step(StepParams p, cudaStream_t st) {
     const SelectiveArgs& a = p.a;
     const int per_cta = kStepThreads / p.L;
     p.cblocks = (a.D + per_cta - 1) / per_cta;
-    // Four batch rows a thread once that leaves every SM some CTAs; fewer rows finish sooner one each.
-    constexpr int RB = KP <= 4 ? 4 : 2;
-    const bool many = p.cblocks * ((a.b + RB - 1) / RB) >= 2 * 148;
-    const int64_t blocks = p.cblocks * (many ? (a.b + RB - 1) / RB : a.b);
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    if (many)
-        step_kernel<E, Td, V, KP, RB><<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
-    else
-        step_kernel<E, Td, V, KP, 1><<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
-    return cudaGetLastError();
+    // Several batch rows a thread once that leaves every SM some CTAs; fewer rows finish sooner one each.
+    constexpr int R = V * KP <= 4 ? 4 : 2;
+    const int64_t grouped = p.cblocks * ((a.b + R - 1) / R);
+    return grouped >= 4 * 148 ? launch_rows<E, Td, V, KP, R>(p, grouped, st)
+                              : launch_rows<E, Td, V, KP, 1>(p, p.cblocks * a.b, st);
 }
 
 template <typename E, typename Td>
@@ -670,6 +724,7 @@ cudaError_t step_any(const SelectiveArgs& a, cudaStream_t st) {
     auto ok = [](const void* q, const ssd_strides_t& s) {
         return aligned(q, 4 * sizeof(E)) && s.batch % 4 == 0 && s.row % 4 == 0;
     };
+    p.a_wide = aligned(a.A, 16);
     p.bc_wide = ok(a.B, a.Bs) && ok(a.C, a.Cs);
     const int64_t kp = (pieces + p.L - 1) / p.L;
     if (wide) return kp == 1 ? launch_step<E, Td, 4, 1>(p, st) : launch_step<E, Td, 4, 2>(p, st);
