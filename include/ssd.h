@@ -407,10 +407,11 @@ SSD_API ssd_status_t ssd_causal_conv1d_step(const ssd_conv_shape_t* shape, const
 typedef struct {
     int64_t batch;        /* b >= 0                                          */
     int64_t seqlen;       /* T >= 0, at most 2^31 - 2^16                     */
-    int64_t channels;     /* D >= 1                                          */
+    int64_t channels;     /* D >= 1, below 2^31                              */
     int64_t ngroups;      /* G >= 1, divides D                               */
     int64_t dstate;       /* N in [1, 256]                                   */
-    ssd_strides_t u, dt, z, B, C;   /* strides of the inputs (z's unused without z) */
+    ssd_strides_t u, dt, z, B, C;   /* strides of the inputs (z's unused without z), */
+                                    /* rows below 2^31 elements apart                */
     int32_t dtype;        /* ssd_dtype_t of u, z, B, C and y                 */
     int32_t dt_dtype;     /* ssd_dtype_t of dt: SSD_F32 or dtype             */
     int32_t dt_softplus;  /* 0 or 1                                          */

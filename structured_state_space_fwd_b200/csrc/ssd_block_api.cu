@@ -17,7 +17,8 @@ using ssd::Range;
 
 constexpr int64_t kMaxState = 256;
 constexpr int64_t kMaxDocs = 1 << 24;
-constexpr int64_t kMaxTokens = 0x7fff0000;   // token counts of the scan's kernels are 32-bit
+constexpr int64_t kMaxTokens = 0x7fff0000;   // tokens and rows of the scan's kernels are 32-bit
+constexpr int64_t kMaxRow = 0x7fffffff;      // numbers, so that an offset is one 32 x 32 product
 constexpr double kMaxElems = 4.0e15;      // keeps every element index well inside int64
 
 size_t elem_size(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
@@ -125,8 +126,11 @@ ssd_status_t check_selective_shape(const ssd_selective_shape_t* s) {
         (double)s->batch * (double)s->seqlen * (double)s->ngroups * (double)s->dstate > kMaxElems ||
         (double)s->batch * (double)s->channels * (double)s->dstate > kMaxElems)
         return SSD_ERR_UNSUPPORTED;
-    for (const ssd_strides_t* p : {&s->u, &s->dt, &s->B, &s->C})
+    if (s->channels > kMaxRow) return SSD_ERR_UNSUPPORTED;
+    for (const ssd_strides_t* p : {&s->u, &s->dt, &s->B, &s->C}) {
         if (!stride_ok(*p, s->batch, s->seqlen)) return SSD_ERR_INVALID_ARG;
+        if (p->row > kMaxRow) return SSD_ERR_UNSUPPORTED;
+    }
     return SSD_OK;
 }
 
@@ -136,6 +140,7 @@ ssd_status_t check_selective(const ssd_selective_shape_t* s, int64_t nseq, const
                              const float* dt_bias, const int32_t* cu, const float* init, void* y, float* fin,
                              bool in_place, ssd::SelectiveArgs* a) {
     if (z && !stride_ok(s->z, s->batch, s->seqlen)) return SSD_ERR_INVALID_ARG;
+    if (z && s->z.row > kMaxRow) return SSD_ERR_UNSUPPORTED;
     const size_t es = elem_size(s->dtype), des = elem_size(s->dt_dtype);
     const int64_t b = s->batch, T = s->seqlen, Dc = s->channels, GN = s->ngroups * s->dstate;
     const size_t zu = span(s->u, b, T, Dc, es), zdt = span(s->dt, b, T, Dc, des);

@@ -19,7 +19,7 @@
 namespace ssd {
 namespace {
 
-constexpr int kRunWarps = 8;     // token runs per CTA: one per warp, on the same 32 channel vectors
+constexpr int kRunWarps = 4;     // token runs per CTA: one per warp, on the same 32 channel vectors
 constexpr int kBatch = 8;        // tokens whose loads a thread issues together
 
 struct ConvParams {
@@ -168,7 +168,7 @@ __device__ __forceinline__ int64_t find_doc(const int* cu, int64_t n, int64_t t)
 }
 
 template <typename E, int VW, int W, bool kPacked, bool kSilu>
-__global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kRunWarps * 32, sizeof(E) == 2 ? 5 : 4) conv_kernel(const ConvParams p) {
     using Raw = typename Pack<E, VW>::T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t blk = blockIdx.x;
@@ -232,23 +232,35 @@ __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p
         }
     };
     open(t0);
-    auto one = [&](int64_t t, const Raw& raw) {
-        const Vec<VW> x = widen(raw);
+    // Addresses are walked: a product of 64-bit strides for every row costs more than its arithmetic.
+    const E* ut = u + t0 * p.ur;
+    E* yt = out.y + t0 * out.stride;
+    const int64_t ys = out.stride;
+    auto one = [&](E* to, const Vec<VW>& x) {
         Raw o;
         narrow(taps.template apply<kSilu>(window, x), o);
         push<W>(window, x);
-        __stcs(reinterpret_cast<Raw*>(out.y + t * out.stride), o);
+        __stcs(reinterpret_cast<Raw*>(to), o);
     };
-    int64_t t = t0;
-    for (; t + kBatch <= t1; t += kBatch) {
-        Raw raw[kBatch];
+    // Whole batches, the next one's loads in flight while this one is computed; the rest, and from
+    // the batch in which a document starts, token by token.
+    const int64_t whole = kPacked && next < t1 ? next : t1;
+    int left = (int)(whole > t0 ? whole - t0 : 0), tokens = (int)(t1 - t0);
+    Raw raw[kBatch];
+    auto fetch = [&]() {
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) raw[i] = __ldcs(reinterpret_cast<const Raw*>(u + (t + i) * p.ur));
-        if (kPacked && t + kBatch > next) break;             // a document starts among these
+        for (int i = 0; i < kBatch; ++i, ut += p.ur) raw[i] = __ldcs(reinterpret_cast<const Raw*>(ut));
+    };
+    if (left >= kBatch) fetch();
+    for (; left >= kBatch; left -= kBatch, tokens -= kBatch) {
+        Vec<VW> x[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) one(t + i, raw[i]);
+        for (int i = 0; i < kBatch; ++i) x[i] = widen(raw[i]);
+        if (left >= 2 * kBatch) fetch();
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i, yt += ys) one(yt, x[i]);
     }
-    for (; t < t1; ++t) {
+    for (int64_t t = t1 - tokens; t < t1; ++t, ut += p.ur, yt += ys) {
         if constexpr (kPacked) {
             if (t >= next && seq + 1 < p.nseq) {             // a document starts here: the last that does
                 do {
@@ -259,7 +271,7 @@ __global__ void __launch_bounds__(kRunWarps * 32) conv_kernel(const ConvParams p
                 open(t);
             }
         }
-        one(t, *reinterpret_cast<const Raw*>(u + t * p.ur));
+        one(yt, widen(*reinterpret_cast<const Raw*>(ut)));
     }
 }
 

@@ -28,6 +28,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "ssd_block.cuh"
 #include "ssd_internal.h"
@@ -84,21 +85,21 @@ __device__ __forceinline__ void pair_wait(int id) {
 // below `rows` or the column not below `cols`. wide: in 16-byte pieces (a piece is then inside or
 // outside as a whole).
 template <int K, int W, typename E>
-__device__ __forceinline__ void stage(E* dst, const E* src, int64_t row, int rows, int cols, int lane, bool wide) {
+__device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, int cols, int lane, bool wide) {
     constexpr int V = 16 / sizeof(E), P = W >= V ? W / V : 1, kPieces = (K * P + 31) / 32;
     if (W >= V && wide) {
         const int k0 = lane / P, c = (lane % P) * V;
-        const E* from = src + k0 * row + c;
+        const E* from = src + ((int64_t)k0 * row + c);
         if (rows == K && cols >= W) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                if (K * P % 32 == 0 || k0 < K) copy16(dst + (k0 + i * (32 / P)) * W + c, from + i * (32 / P) * row, true);
+                if (K * P % 32 == 0 || k0 < K) copy16(dst + (k0 + i * (32 / P)) * W + c, from + (int64_t)(i * (32 / P)) * row, true);
         } else {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int k = k0 + i * (32 / P);
                 const bool ok = k < rows && c < cols;
-                if (K * P % 32 == 0 || k < K) copy16(dst + k * W + c, ok ? from + i * (32 / P) * row : src, ok);
+                if (K * P % 32 == 0 || k < K) copy16(dst + k * W + c, ok ? from + (int64_t)(i * (32 / P)) * row : src, ok);
             }
         }
     } else {
@@ -107,9 +108,9 @@ __device__ __forceinline__ void stage(E* dst, const E* src, int64_t row, int row
             const int k = idx / W, c = idx % W;
             const bool ok = k < rows && c < cols;
             if constexpr (sizeof(E) == 4) {
-                copy4(dst + idx, ok ? src + k * row + c : src, ok);
+                copy4(dst + idx, ok ? src + ((int64_t)k * row + c) : src, ok);
             } else {
-                dst[idx] = ok ? src[k * row + c] : E(0.f);
+                dst[idx] = ok ? src[(int64_t)k * row + c] : E(0.f);
             }
         }
     }
@@ -238,21 +239,24 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
     const E* const zb = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d0 : nullptr;
     const E* const Bb = static_cast<const E*>(a.B) + b * a.Bs.batch + g * N;
     const E* const Cb = static_cast<const E*>(a.C) + b * a.Cs.batch + g * N;
+    const int ur = (int)a.us.row, dtr = (int)a.dts.row, zr = (int)a.zs.row, Br = (int)a.Bs.row, Cr = (int)a.Cs.row;
     // the copies of the tile at token t, state block nb; u, dt, z (stage sr) with the first block
     auto issue = [&](int t, int nb, int sr, int sb) {
         const int n = min(t1 - t, K);
         if (n > 0) {
             if (nb == 0) {
-                stage<K, CH>(&m.u[sr][0][0], ub + t * a.us.row, a.us.row, n, cols, lane, p.rows16);
-                stage<K, CH>(&m.dt[sr][0][0], dtb + t * a.dts.row, a.dts.row, n, cols, lane, p.rows16);
-                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + t * a.zs.row, a.zs.row, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
+                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
             }
-            stage<K, NS>(&m.B[sb][0][0], Bb + t * a.Bs.row + nb * NS, a.Bs.row, n, N - nb * NS, lane, p.bc16);
-            stage<K, NS>(&m.C[sb][0][0], Cb + t * a.Cs.row + nb * NS, a.Cs.row, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc16);
         }
         copy_commit();
     };
 
+    E* const yb = static_cast<E*>(a.y) + b * a.T * a.D + d0 + 2 * cp;
+    const int64_t Dr = a.D;
     // Cut: all warps take part in every round of W tiles, those past the end too, which pass the
     // states on. Alternating: a warp takes every second tile.
     const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
@@ -422,9 +426,9 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
 #pragma unroll
             for (int q = 0; q < K; ++q) r[q] = yv[q];
         }
-        E* to = static_cast<E*>(a.y) + (b * a.T + t + j) * a.D + d0 + 2 * cp;
+        E* to = yb + (int64_t)(t + j) * (int)Dr;
 #pragma unroll
-        for (int q = 0; q < K / SL; ++q, to += SL * a.D) {
+        for (int q = 0; q < K / SL; ++q, to += SL * Dr) {
             const int k = q * SL + j;
             float2 v = __ffma2_rn(skip, pair_of(&m.u[sr][k][2 * cp]), r[q]);
             if (zb) {
@@ -513,7 +517,7 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
 // ---- decoding --------------------------------------------------------------
 //
 // One or a few tokens per sequence from a state in HBM: the state's 8 b D N bytes bound it. L lanes
-// share a channel, V states a lane and piece; a thread keeps the pieces of kRows batch rows of its
+// share a channel, V states a lane and piece; a thread keeps the pieces of R batch rows of its
 // channel in registers for all of the call's tokens, so that A (as large as one row's state) is read
 // once for them and their loads are in flight together. What a (row, channel) needs once - the step,
 // dt u, the gate - is computed by one of the L lanes and handed to the others; the rows' sums are
@@ -527,67 +531,72 @@ struct StepParams {
     bool a_wide, bc_wide;        // A (B and C) take loads of V elements
 };
 
-template <int V>
-__device__ __forceinline__ void load_bc(const float* p, bool wide, float (&v)[V]) {
-    if (V == 4 && wide) {
-        const float4 q = *reinterpret_cast<const float4*>(p);
-        v[0] = q.x; v[1 % V] = q.y; v[2 % V] = q.z; v[3 % V] = q.w;
-    } else {
+// V elements as they lie in memory
+template <typename E, int V>
+struct alignas(V * sizeof(E)) Piece {
+    E v[V];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = p[i];
+        for (int i = 0; i < V; ++i) v[i] = E(0.f);
     }
-}
-template <int V>
-__device__ __forceinline__ void load_bc(const __nv_bfloat16* p, bool wide, float (&v)[V]) {
-    if (V == 4 && wide) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p);
-        v[0] = bf16_lo(q.x); v[1 % V] = bf16_hi(q.x); v[2 % V] = bf16_lo(q.y); v[3 % V] = bf16_hi(q.y);
-    } else {
+    __device__ __forceinline__ void load(const E* p, bool wide) {
+        if (V == 4 && wide) {
+            if constexpr (sizeof(E) == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+            else *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_float(p[i]);
+            for (int i = 0; i < V; ++i) v[i] = p[i];
+        }
     }
+    __device__ __forceinline__ void widen(float2 (&f)[2]) const { f[0] = pair_of(v); f[1] = pair_of(v + 2 % V); }
+    __device__ __forceinline__ void widen(float (&f)[1]) const { f[0] = to_float(v[0]); }
+};
+__device__ __forceinline__ void load_piece(const float* p, float2 (&v)[2]) {
+    const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
+    v[0] = make_float2(q.x, q.y);
+    v[1] = make_float2(q.z, q.w);
 }
-template <int V>
-__device__ __forceinline__ void load_piece(const float* p, float (&v)[V]) {
-    if constexpr (V == 4) {
-        const float4 q = __ldcs(reinterpret_cast<const float4*>(p));
-        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-    } else {
-        v[0] = __ldcs(p);
-    }
+__device__ __forceinline__ void load_piece(const float* p, float (&v)[1]) { v[0] = __ldcs(p); }
+__device__ __forceinline__ void store_piece(float* p, const float2 (&v)[2]) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
 }
-template <int V>
-__device__ __forceinline__ void store_piece(float* p, const float (&v)[V]) {
-    if constexpr (V == 4) {
-        __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    } else {
-        __stcs(p, v[0]);
-    }
-}
+__device__ __forceinline__ void store_piece(float* p, const float (&v)[1]) { __stcs(p, v[0]); }
 
 // R rows a thread, Q = R / (lanes that prepare them): a lane prepares rows q (R / Q) + j, q < Q.
+// Addresses are walked: a row or token further costs an addition, where a product of 64-bit
+// strides costs several instructions and made up half of the kernel's.
 template <typename E, typename Td, int V, int KP, int R, int Q>
-__global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constant__ StepParams p) {
+__global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
+    step_kernel(const __grid_constant__ StepParams p) {
     constexpr int PL = R / Q;                            // lanes that prepare rows, at most L
+    constexpr int M = V == 4 ? 2 : 1;                    // packed values of a piece
+    using F = typename std::conditional<V == 4, float2, float>::type;
     const SelectiveArgs& a = p.a;
     const int L = p.L, j = threadIdx.x & (L - 1), N = (int)a.N;
     const int64_t d = blockIdx.x % p.cblocks * (kStepThreads / L) + threadIdx.x / L;
     const int64_t b0 = blockIdx.x / p.cblocks * R;
     const bool live = d < a.D;                           // whole groups of L lanes
-    const int64_t dc = live ? d : 0, g = dc / (a.D / a.G);
+    const int64_t dc = live ? d : 0;
     const int rows = live ? (int)min(a.b - b0, (int64_t)R) : 0;
-    float h[R][KP][V], A[KP][V];
-    float* const state = a.fin + (b0 * a.D + dc) * N + j * V;
+    bool in[KP];
+#pragma unroll
+    for (int k = 0; k < KP; ++k) in[k] = (j + k * L) * V < N;
+
+    F h[R][KP][M], A[KP][M];
     const int64_t next_row = a.D * N;
+    float* const state = a.fin + (b0 * a.D + dc) * N + j * V;
+    {
+        const float* s = state;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r, s += next_row)
 #pragma unroll
-        for (int k = 0; k < KP; ++k) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[r][k][i] = 0.f;
-            if (r < rows && (j + k * L) * V < N) load_piece<V>(state + r * next_row + k * L * V, h[r][k]);
-        }
-    // the rows this lane prepares (j % PL: with more lanes than rows the others repeat them)
+            for (int k = 0; k < KP; ++k) {
+                h[r][k][0] = h[r][k][M - 1] = all<F>(0.f);
+                if (r < rows && in[k]) load_piece(s + k * L * V, h[r][k]);
+            }
+    }
+    // the rows this lane prepares (with more lanes than rows the others repeat them); an absent row
+    // reads the first's inputs
     const int own = j % PL;
     const Td* dtp[Q];
     const E* up[Q];
@@ -599,57 +608,76 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
         up[q] = static_cast<const E*>(a.u) + b * a.us.batch + dc;
         zp[q] = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + dc : nullptr;
     }
-    const E* Bp = static_cast<const E*>(a.B) + b0 * a.Bs.batch + g * N + j * V;
-    const E* Cp = static_cast<const E*>(a.C) + b0 * a.Cs.batch + g * N + j * V;
+    const int64_t g = a.G > 1 ? dc / (a.D / a.G) : 0;
+    const E* Bt = static_cast<const E*>(a.B) + b0 * a.Bs.batch + g * N + j * V;
+    const E* Ct = static_cast<const E*>(a.C) + b0 * a.Cs.batch + g * N + j * V;
 #pragma unroll
     for (int k = 0; k < KP; ++k) {
-        float v[V];
+        Piece<float, V> q;
+        q.zero();
+        if (in[k]) q.load(a.A + dc * N + (j + k * L) * V, p.a_wide);
+        q.widen(A[k]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = 0.f;
-        if ((j + k * L) * V < N) load_bc<V>(a.A + dc * N + (j + k * L) * V, p.a_wide, v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) A[k][i] = v[i] * kLog2e;
+        for (int m = 0; m < M; ++m) A[k][m] = mul_(A[k][m], all<F>(kLog2e));
     }
     const float skip = a.Dskip ? a.Dskip[dc] : 0.f, bias = a.dt_bias ? a.dt_bias[dc] : 0.f;
     E* y = static_cast<E*>(a.y) + (b0 + own) * a.T * a.D + dc;
-    for (int64_t t = 0; t < a.T; ++t) {
-        float dt[Q], u[Q], z[Q], acc[R];
+    for (int64_t t = 0; t < a.T; ++t, y += a.D) {
+        float dt[Q], u[Q], gate[Q], acc[R];
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            dt[q] = to_float(dtp[q][t * a.dts.row]);
-            u[q] = to_float(up[q][t * a.us.row]);
-            z[q] = a.z ? to_float(zp[q][t * a.zs.row]) : 0.f;
+            dt[q] = to_float(*dtp[q]);
+            u[q] = to_float(*up[q]);
+            gate[q] = a.z ? to_float(*zp[q]) : 0.f;
+            dtp[q] += a.dts.row;
+            up[q] += a.us.row;
+            zp[q] += a.zs.row;
         }
-        // all of B and C before the first use
-        float Bv[R][KP][V], Cv[R][KP][V];
+        Piece<E, V> Bv[R][KP], Cv[R][KP];                // all of B and C before the first use
+        {
+            const E* B = Bt;
+            const E* C = Ct;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
 #pragma unroll
-            for (int k = 0; k < KP; ++k) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) Bv[r][k][i] = Cv[r][k][i] = 0.f;
-                if (r < rows && (j + k * L) * V < N) {
-                    load_bc<V>(Bp + r * a.Bs.batch + t * a.Bs.row + k * L * V, p.bc_wide, Bv[r][k]);
-                    load_bc<V>(Cp + r * a.Cs.batch + t * a.Cs.row + k * L * V, p.bc_wide, Cv[r][k]);
+                for (int k = 0; k < KP; ++k) {
+                    Bv[r][k].zero();
+                    Cv[r][k].zero();
+                    if (r < rows && in[k]) {
+                        Bv[r][k].load(B + k * L * V, p.bc_wide);
+                        Cv[r][k].load(C + k * L * V, p.bc_wide);
+                    }
                 }
+                B += a.Bs.batch;
+                C += a.Cs.batch;
             }
+            Bt += a.Bs.row;
+            Ct += a.Cs.row;
+        }
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             dt[q] += bias;
             if (a.softplus) dt[q] = softplus(dt[q]);
+            gate[q] = a.z ? silu(gate[q]) : 1.f;
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             const float dtr = __shfl_sync(0xffffffffu, dt[r / PL], r % PL, L);
             const float du = dtr * __shfl_sync(0xffffffffu, u[r / PL], r % PL, L);
-            acc[r] = 0.f;
+            F sum = all<F>(0.f);
 #pragma unroll
-            for (int k = 0; k < KP; ++k)
+            for (int k = 0; k < KP; ++k) {
+                F Bf[M], Cf[M];
+                Bv[r][k].widen(Bf);
+                Cv[r][k].widen(Cf);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    h[r][k][i] = fmaf(ex2(dtr * A[k][i]), h[r][k][i], du * Bv[r][k][i]);
-                    acc[r] = fmaf(Cv[r][k][i], h[r][k][i], acc[r]);
+                for (int m = 0; m < M; ++m) {
+                    h[r][k][m] = fma_(ex2(mul_(A[k][m], all<F>(dtr))), h[r][k][m], mul_(Bf[m], all<F>(du)));
+                    sum = fma_(Cf[m], h[r][k][m], sum);
                 }
+            }
+            if constexpr (V == 4) acc[r] = sum.x + sum.y;
+            else acc[r] = sum;
         }
         // lane j ends with the sums of the rows q PL + j % PL
         float sum[Q];
@@ -673,17 +701,15 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
             for (int q = 0; q < Q; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], off);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            if (j < PL && q * PL + own < rows) {
-                float v = fmaf(skip, u[q], sum[q]);
-                if (a.z) v *= silu(z[q]);
-                store_elem(y + (q * PL * a.T + t) * a.D, v);
-            }
+            if (j < PL && q * PL + own < rows)
+                store_elem(y + q * PL * a.T * a.D, fmaf(skip, u[q], sum[q]) * gate[q]);
     }
+    float* s = state;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < R; ++r, s += next_row)
 #pragma unroll
         for (int k = 0; k < KP; ++k)
-            if (r < rows && (j + k * L) * V < N) store_piece<V>(state + r * next_row + k * L * V, h[r][k]);
+            if (r < rows && in[k]) store_piece(s + k * L * V, h[r][k]);
 }
 
 template <typename E, typename Td, int V, int KP, int R>
