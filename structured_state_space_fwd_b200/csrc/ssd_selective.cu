@@ -116,7 +116,7 @@ __device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, i
     }
 }
 
-// A warp's shared memory: two stages of raw inputs, the tile's (dt, dt u), and B, C in fp32.
+// A warp's shared memory: two stages of inputs, and the tile's (dt, dt u).
 template <typename E, typename Td, int SL, int K>
 struct WarpMem {
     static constexpr int CH = 64 / SL, NS = 4 * SL;
@@ -126,8 +126,6 @@ struct WarpMem {
     alignas(16) E B[2][K][NS];
     alignas(16) E C[2][K][NS];
     alignas(16) float4 s[K][CH / 2];          // dt, dt u of two channels
-    alignas(16) float Bf[sizeof(E) == 2 ? K : 1][NS];
-    alignas(16) float Cf[sizeof(E) == 2 ? K : 1][NS];
 };
 
 // Two neighbouring elements.
@@ -140,17 +138,16 @@ __device__ __forceinline__ void store_pair(float* p, float2 v) { *reinterpret_ca
 __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
 }
-template <int K, int NS>
-__device__ __forceinline__ void widen(float (*dst)[NS], const __nv_bfloat16 (*src)[NS], int lane) {
-#pragma unroll
-    for (int i = 0; i < (K * NS + 127) / 128; ++i) {
-        const int at = (lane + 32 * i) * 4;
-        if (K * NS % 128 == 0 || at < K * NS) {
-            const uint2 q = *reinterpret_cast<const uint2*>(&src[0][0] + at);
-            *reinterpret_cast<float4*>(&dst[0][0] + at) =
-                make_float4(bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y));
-        }
-    }
+// Four neighbouring elements as two pairs.
+__device__ __forceinline__ void quad_of(const float* p, float2 (&v)[2]) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = make_float2(q.x, q.y);
+    v[1] = make_float2(q.z, q.w);
+}
+__device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2 (&v)[2]) {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
+    v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
 }
 
 // 2 x 4 states of a lane (or their decays): [channel of the pair][pair of states]
@@ -262,7 +259,29 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
     const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
     const int rounds = (tiles + W - 1) / W;
     const int mine = kCut ? rounds : (tiles - warp + W - 1) / W;
-    float2 yv[K];
+    // y of a pair of channels: the lane's parts, and, summed over the SL lanes that share the pair by
+    // exchanges of SL tokens each, the tokens q SL + j that the lane finishes
+    constexpr int kHeld = kCut ? K : SL;
+    float2 yv[kHeld], ysum[K / SL] = {};
+    auto give = [&](float2 v, int mask) {
+        return make_float2(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask));
+    };
+    auto gather = [&](int q) {
+        const float2* const v = yv + q * SL % kHeld;
+        float2 r;
+        if constexpr (SL == 4) {
+            const bool up = j & 2, odd = j & 1;
+            const float2 lo = add_(up ? v[2] : v[0], give(up ? v[0] : v[2], 2 * CL));
+            const float2 hi = add_(up ? v[3] : v[1], give(up ? v[1] : v[3], 2 * CL));
+            r = add_(odd ? hi : lo, give(odd ? lo : hi, CL));
+        } else if constexpr (SL == 2) {
+            const bool odd = j & 1;
+            r = add_(odd ? v[1] : v[0], give(odd ? v[0] : v[1], CL));
+        } else {
+            r = v[0];
+        }
+        ysum[q] = add_(ysum[q], r);
+    };
     States A;
     auto rates = [&](int nb) {
         row_of(a.A, da, nb, kLog2e, A.v[0][0], A.v[0][1]);
@@ -288,25 +307,28 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
                 if (nb == 0) {
                     // once per (token, channel): the step and dt u; past the end both are 0, which
                     // leaves the state as it is
+                    float2 v[K / SL];
 #pragma unroll
-                    for (int q = 0; q < K / SL; ++q) {
-                        const int k = q * SL + j;
-                        float2 v = pair_of(&m.dt[sr][k][2 * cp]);
-                        const float2 u = pair_of(&m.u[sr][k][2 * cp]);
-                        v = __fadd2_rn(v, bias);
-                        if (a.softplus) v = softplus(v);
-                        v = k < n ? v : both(0.f);
-                        const float2 du = __fmul2_rn(v, u);
-                        m.s[k][cp] = make_float4(v.x, du.x, v.y, du.y);
+                    for (int q = 0; q < K / SL; ++q) v[q] = add_(pair_of(&m.dt[sr][q * SL + j][2 * cp]), bias);
+                    if (a.softplus) {
+#pragma unroll
+                        for (int q = 0; q < K / SL; ++q) v[q] = softplus(v[q]);
+                    }
+                    if (n < K) {
+#pragma unroll
+                        for (int q = 0; q < K / SL; ++q) v[q] = q * SL + j < n ? v[q] : both(0.f);
                     }
 #pragma unroll
-                    for (int k = 0; k < K; ++k) yv[k] = both(0.f);
-                }
-                if constexpr (sizeof(E) == 2) {
-                    widen<K, NS>(m.Bf, m.B[sb], lane);
-                    widen<K, NS>(m.Cf, m.C[sb], lane);
+                    for (int q = 0; q < K / SL; ++q) {
+                        const float2 du = mul_(v[q], pair_of(&m.u[sr][q * SL + j][2 * cp]));
+                        m.s[q * SL + j][cp] = make_float4(v[q].x, du.x, v[q].y, du.y);
+                    }
                 }
                 __syncwarp();
+            }
+            if (nb == 0) {
+#pragma unroll
+                for (int q = 0; q < K / SL; ++q) ysum[q] = both(0.f);
             }
             States h, decay;
             float2 gc[kCut ? K : 1][2][2];               // C_t times the decays up to t
@@ -319,41 +341,47 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
                 h.load(carry + nb * 64 + lane);
             }
             if (n > 0) {
-                const float* Bt;
-                const float* Ct;
-                if constexpr (sizeof(E) == 2) {
-                    Bt = &m.Bf[0][0] + j * 4;
-                    Ct = &m.Cf[0][0] + j * 4;
-                } else {
-                    Bt = &m.B[sb][0][0] + j * 4;
-                    Ct = &m.C[sb][0][0] + j * 4;
-                }
+                const E* const Bt = &m.B[sb][0][0] + j * 4;
+                const E* const Ct = &m.C[sb][0][0] + j * 4;
+                // exps of the next token ahead of the states of this one
+                float2 e[2][2][2];
+                float4 sk = m.s[0][cp];
+                auto exps = [&](float2 (&to)[2][2], const float4& s) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) to[c][i] = ex2(mul_(both(c ? s.z : s.x), A.v[c][i]));
+                };
+                exps(e[0], sk);
 #pragma unroll
                 for (int k = 0; k < K; ++k) {
-                    const float4 s = m.s[k][cp];
-                    const float4 Bk = *reinterpret_cast<const float4*>(Bt + k * NS);
-                    const float4 Ck = *reinterpret_cast<const float4*>(Ct + k * NS);
-                    const float2 Bv[2] = {make_float2(Bk.x, Bk.y), make_float2(Bk.z, Bk.w)};
-                    const float2 Cv[2] = {make_float2(Ck.x, Ck.y), make_float2(Ck.z, Ck.w)};
+                    const float4 s = sk;
+                    float2 Bv[2], Cv[2];
+                    quad_of(Bt + k * NS, Bv);
+                    quad_of(Ct + k * NS, Cv);
+                    if (k + 1 < K) {
+                        sk = m.s[k + 1][cp];
+                        exps(e[(k + 1) & 1], sk);
+                    }
                     float part[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float2 st = both(c ? s.z : s.x), du = both(c ? s.w : s.y);
+                        const float2 du = both(c ? s.w : s.y);
                         float2 r = both(0.f);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float2 e = __fmul2_rn(st, A.v[c][i]);
-                            e = ex2(e);
-                            h.v[c][i] = __ffma2_rn(e, h.v[c][i], __fmul2_rn(du, Bv[i]));
-                            r = i ? __ffma2_rn(Cv[i], h.v[c][i], r) : __fmul2_rn(Cv[i], h.v[c][i]);
+                            const float2 ek = e[k & 1][c][i];
+                            h.v[c][i] = fma_(ek, h.v[c][i], mul_(du, Bv[i]));
+                            r = i ? fma_(Cv[i], h.v[c][i], r) : mul_(Cv[i], h.v[c][i]);
                             if constexpr (kCut) {
-                                decay.v[c][i] = k ? __fmul2_rn(decay.v[c][i], e) : e;
-                                gc[k][c][i] = __fmul2_rn(Cv[i], decay.v[c][i]);
+                                decay.v[c][i] = k ? mul_(decay.v[c][i], ek) : ek;
+                                gc[k][c][i] = mul_(Cv[i], decay.v[c][i]);
                             }
                         }
                         part[c] = r.x + r.y;
                     }
-                    yv[k] = __fadd2_rn(yv[k], make_float2(part[0], part[1]));
+                    yv[k % kHeld] = make_float2(part[0], part[1]);
+                    if (!kCut && k % SL == SL - 1) gather(k / SL);
                 }
             }
             if constexpr (kCut) {
@@ -373,7 +401,7 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) h.v[c][i] = __ffma2_rn(decay.v[c][i], in.v[c][i], h.v[c][i]);
+                    for (int i = 0; i < 2; ++i) h.v[c][i] = fma_(decay.v[c][i], in.v[c][i], h.v[c][i]);
                 if (warp + 1 < W) {
                     h.store(slot + 64);
                     if (NB == 1) pair_arrive<W>(warp + 1);
@@ -389,10 +417,11 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             const float2 r =
-                                __ffma2_rn(gc[k][c][1], in.v[c][1], __fmul2_rn(gc[k][c][0], in.v[c][0]));
+                                fma_(gc[k][c][1], in.v[c][1], mul_(gc[k][c][0], in.v[c][0]));
                             part[c] = r.x + r.y;
                         }
-                        yv[k] = __fadd2_rn(yv[k], make_float2(part[0], part[1]));
+                        yv[k % kHeld] = add_(yv[k % kHeld], make_float2(part[0], part[1]));
+                        if (k % SL == SL - 1) gather(k / SL);
                     }
                 }
             } else {
@@ -401,48 +430,24 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
             }
         }
         if (n <= 0) continue;
-        // sums over the SL lanes of a pair: after the exchanges lane j holds tokens k with k % SL == j
-        float2 r[K / SL];
-        auto give = [&](float2 v, int mask) {
-            return make_float2(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask));
-        };
-        if constexpr (SL == 4) {
-            float2 half[K / 2];
-            const bool up = j & 2, odd = j & 1;
+        E* to = yb + (int64_t)(t + j) * (int)Dr;
+        const int64_t step = SL * Dr;
 #pragma unroll
-            for (int q = 0; q < K / 2; ++q) {
-                const int k = (q / 2) * 4 + q % 2;       // bit 1 clear; k + 2 has it set
-                half[q] = __fadd2_rn(up ? yv[k + 2] : yv[k], give(up ? yv[k] : yv[k + 2], 2 * CL));
-            }
+        for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+        if (zb) {
 #pragma unroll
-            for (int q = 0; q < K / 4; ++q)
-                r[q] = __fadd2_rn(odd ? half[2 * q + 1] : half[2 * q], give(odd ? half[2 * q] : half[2 * q + 1], CL));
-        } else if constexpr (SL == 2) {
-            const bool odd = j & 1;
+            for (int q = 0; q < K / SL; ++q) ysum[q] = mul_(ysum[q], silu(pair_of(&m.z[sr][q * SL + j][2 * cp])));
+        }
+        if (n == K && cols == CH && p.y_pairs) {
 #pragma unroll
-            for (int q = 0; q < K / 2; ++q)
-                r[q] = __fadd2_rn(odd ? yv[2 * q + 1] : yv[2 * q], give(odd ? yv[2 * q] : yv[2 * q + 1], CL));
+            for (int q = 0; q < K / SL; ++q, to += step) store_pair(to, ysum[q]);
         } else {
 #pragma unroll
-            for (int q = 0; q < K; ++q) r[q] = yv[q];
-        }
-        E* to = yb + (int64_t)(t + j) * (int)Dr;
-#pragma unroll
-        for (int q = 0; q < K / SL; ++q, to += SL * Dr) {
-            const int k = q * SL + j;
-            float2 v = __ffma2_rn(skip, pair_of(&m.u[sr][k][2 * cp]), r[q]);
-            if (zb) {
-                const float2 z = pair_of(&m.z[sr][k][2 * cp]);
-                v = __fmul2_rn(v, silu(z));
-            }
-            if (k < n) {
-                if (p.y_pairs && in1) {
-                    store_pair(to, v);
-                } else {
-                    if (in0) store_elem(to, v.x);
-                    if (in1) store_elem(to + 1, v.y);
+            for (int q = 0; q < K / SL; ++q, to += step)
+                if (q * SL + j < n) {
+                    if (in0) store_elem(to, ysum[q].x);
+                    if (in1) store_elem(to + 1, ysum[q].y);
                 }
-            }
         }
     }
     copy_wait<0>();
