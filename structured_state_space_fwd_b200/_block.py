@@ -9,7 +9,6 @@ current stream unless `stream` is given.
 from __future__ import annotations
 
 import struct
-from typing import NamedTuple
 
 import torch
 
@@ -22,11 +21,6 @@ _F32 = torch.float32
 # the rest of a decoding step's call
 _conv_shape = struct.Struct("=9q2i").pack
 _selective_shape = struct.Struct("=15q4i").pack
-
-
-class Strides(NamedTuple):
-    batch: int
-    row: int
 
 
 def _refuse(t, name, shape, dtype, device, inner):
@@ -79,12 +73,6 @@ def _first(t, name, dim):
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
 
 
-def _strides(t):
-    """(batch, row) strides; those of dimensions of one or no element do not matter."""
-    s, n = t.stride(), t.shape
-    return Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
-
-
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -95,23 +83,26 @@ def _current_stream(device):
 
 # the raw handle of the device's current stream, without the Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _entries = {}
 
 
-def _call(name, device, stream, *args):
+def _call(name, t, stream, *args):
+    """The entry point on t's device and its current stream, or on `stream`."""
     fn = _entries.get(name)
     if fn is None:
         fn = _entries[name] = getattr(lib(), name)
+    index = t.get_device()
     if stream is None:
-        handle = _raw_stream(device.index) if _raw_stream is not None else _current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        handle = _raw_stream(index) if _raw_stream is not None else _current_stream(t.device)
+    elif stream.device != t.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
     else:
         handle = stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, handle)
     if st:
         check(st, name)
@@ -134,31 +125,46 @@ def _offsets(cu_seqlens, T, device):
 
 # ---- the short causal convolution ------------------------------------------
 
-def _conv_args(u, weight, bias, silu, split, out):
-    """The width, the checked shape as bytes, the outputs and three pointers to them."""
+def _check_conv(u, weight, bias):
+    """Raises what is wrong with the convolution's inputs."""
     _first(u, "u", 3)
-    b, T, C = u.shape
-    dev = u.device
-    _in(u, "u", u.shape, u.dtype, dev)
+    _in(u, "u", u.shape, u.dtype, u.device)
     if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
         raise ValueError("weight must be [channels, width]")
-    W = weight.shape[1]
-    _whole(weight, "weight", (C, W), torch.float32, dev)
+    _whole(weight, "weight", (u.shape[2], weight.shape[1]), _F32, u.device)
     if bias is not None:
-        _whole(bias, "bias", (C,), torch.float32, dev)
-    sizes = (C,) if split is None else tuple(int(c) for c in split)
+        _whole(bias, "bias", (u.shape[2],), _F32, u.device)
+
+
+def _conv_args(u, weight, bias, silu, split, out):
+    """The width, the checked shape as bytes, the outputs and three pointers to them."""
+    try:       # the checks of _check_conv at once; it says which one failed
+        b, T, C = u.shape
+        s, index = u.stride(), u.get_device()
+        Cw, W = weight.shape
+        good = (index >= 0 and (s[2] == 1 or C == 1) and u.dtype in _DT and Cw == C and weight.dtype is _F32
+                and weight.get_device() == index and weight.is_contiguous()
+                and (bias is None or (bias.dtype is _F32 and bias.shape == (C,) and bias.get_device() == index
+                                      and bias.is_contiguous())))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_conv(u, weight, bias)
+        b, T, C = u.shape
+        s, W = u.stride(), weight.shape[1]
+    sizes = (C,) if split is None else tuple(split)
     if not 1 <= len(sizes) <= 3 or min(sizes) < 0 or sum(sizes) != C:
         raise ValueError(f"split must be up to three sizes that add up to {C}, got {split}")
     if out is None:
-        ys = [torch.empty((b, T, c), dtype=u.dtype, device=dev) for c in sizes]
+        ys = [u.new_empty((b, T, c)) for c in sizes]
     else:
         ys = [out] if split is None else list(out)
         if len(ys) != len(sizes):
             raise ValueError(f"out must be {len(sizes)} tensors")
         for i, (y, c) in enumerate(zip(ys, sizes)):
-            _whole(y, f"out[{i}]", (b, T, c), u.dtype, dev)
+            _whole(y, f"out[{i}]", (b, T, c), u.dtype, u.device)
     pad = (0,) * (3 - len(sizes))
-    shape = _conv_shape(b, T, C, W, *sizes, *pad, *_strides(u), _DT[u.dtype], 1 if silu else 0)
+    shape = _conv_shape(b, T, C, W, *sizes, *pad, s[0], s[1], _DT[u.dtype], 1 if silu else 0)
     return W, shape, ys, [y.data_ptr() for y in ys] + [None] * len(pad)
 
 
@@ -169,7 +175,7 @@ def _conv_states(u, W, nseq, initial_states, return_final_states, final_states):
     if final_states is not None:
         _whole(final_states, "final_states", size, u.dtype, u.device)
     elif return_final_states:
-        final_states = torch.empty(size, dtype=u.dtype, device=u.device)
+        final_states = u.new_empty(size)
     return final_states
 
 
@@ -190,7 +196,7 @@ def ssd_causal_conv1d(u, weight, bias=None, silu: bool = True, split=None, initi
     """
     W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
     fin = _conv_states(u, W, u.shape[0], initial_states, return_final_states, final_states)
-    _call("ssd_causal_conv1d", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
+    _call("ssd_causal_conv1d", u, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), _ptr(initial_states), *yp, _ptr(fin))
     return _conv_result(ys, split, fin, return_final_states)
 
@@ -210,7 +216,7 @@ def ssd_causal_conv1d_varlen(u, weight, bias=None, cu_seqlens=None, silu: bool =
     cu = _offsets(cu_seqlens, u.shape[1], u.device)
     n = cu.numel() - 1
     fin = _conv_states(u, W, n, initial_states, return_final_states, final_states)
-    _call("ssd_causal_conv1d_varlen", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
+    _call("ssd_causal_conv1d_varlen", u, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), cu.data_ptr(), n, _ptr(initial_states), *yp, _ptr(fin))
     return _conv_result(ys, split, fin, return_final_states)
 
@@ -225,7 +231,7 @@ def ssd_causal_conv1d_step(u, weight, bias, state, silu: bool = True, split=None
             out = out.unsqueeze(1) if split is None else [y.unsqueeze(1) for y in out]
     W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
     _whole(state, "state", (u.shape[0], W - 1, u.shape[2]), u.dtype, u.device)
-    _call("ssd_causal_conv1d_step", u.device, stream, shape, u.data_ptr(), weight.data_ptr(),
+    _call("ssd_causal_conv1d_step", u, stream, shape, u.data_ptr(), weight.data_ptr(),
           _ptr(bias), state.data_ptr(), *yp)
     if one:
         ys = [y.squeeze(1) for y in ys]
@@ -234,13 +240,13 @@ def ssd_causal_conv1d_step(u, weight, bias, state, silu: bool = True, split=None
 
 # ---- the selective scan ----------------------------------------------------
 
-def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
-    """The state size, the checked shape as bytes, the input pointers in the C order, and y."""
+def _check_selective(u, dt, A, B, C, D, z, dt_bias):
+    """Raises what is wrong with the scan's inputs."""
     _first(u, "u", 3)
     b, T, Dc = u.shape
     dev, dtype = u.device, u.dtype
     _in(u, "u", u.shape, dtype, dev)
-    if not isinstance(dt, torch.Tensor) or dt.dtype not in (torch.float32, dtype):
+    if not isinstance(dt, torch.Tensor) or dt.dtype not in (_F32, dtype):
         raise TypeError(f"dt must be a float32 or {dtype} tensor")
     _in(dt, "dt", u.shape, dt.dtype, dev)
     if not isinstance(B, torch.Tensor) or B.dim() != 4:
@@ -248,19 +254,51 @@ def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
     G, N = B.shape[2], B.shape[3]
     _in(B, "B", (b, T, G, N), dtype, dev, 2)
     _in(C, "C", (b, T, G, N), dtype, dev, 2)
-    _whole(A, "A", (Dc, N), torch.float32, dev)
+    _whole(A, "A", (Dc, N), _F32, dev)
     if D is not None:
-        _whole(D, "D", (Dc,), torch.float32, dev)
+        _whole(D, "D", (Dc,), _F32, dev)
     if dt_bias is not None:
-        _whole(dt_bias, "dt_bias", (Dc,), torch.float32, dev)
+        _whole(dt_bias, "dt_bias", (Dc,), _F32, dev)
     if z is not None:
         _in(z, "z", u.shape, dtype, dev)
+
+
+def _vector_ok(t, n, index):
+    return t is None or (t.dtype is _F32 and t.shape == (n,) and t.get_device() == index and t.is_contiguous())
+
+
+def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
+    """The state size, the checked shape as bytes, the input pointers in the C order, and y."""
+    try:       # the checks of _check_selective at once; it says which one failed
+        size = u.shape
+        b, T, Dc = size
+        dtype, index = u.dtype, u.get_device()
+        us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
+        shape = B.shape
+        Bb, BT, G, N = shape
+        zs = (0, 0, 1) if z is None else z.stride()
+        good = (index >= 0 and dtype in _DT and (dt.dtype is _F32 or dt.dtype is dtype) and dt.shape == size
+                and dt.get_device() == index and Bb == b and BT == T and C.shape == shape and B.dtype is dtype
+                and C.dtype is dtype and B.get_device() == index and C.get_device() == index
+                and (Dc == 1 or us[2] == ds[2] == zs[2] == 1) and (N == 1 or bs[3] == cs[3] == 1)
+                and (G == 1 or bs[2] == cs[2] == N) and A.dtype is _F32 and A.shape == (Dc, N)
+                and A.get_device() == index and A.is_contiguous() and _vector_ok(D, Dc, index)
+                and _vector_ok(dt_bias, Dc, index)
+                and (z is None or (z.dtype is dtype and z.shape == size and z.get_device() == index)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        good = False
+    if not good:
+        _check_selective(u, dt, A, B, C, D, z, dt_bias)
+        size, dtype = u.shape, u.dtype
+        (b, T, Dc), (G, N) = size, B.shape[2:]
+        us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
+        zs = (0, 0) if z is None else z.stride()
     if y is None:
-        y = torch.empty((b, T, Dc), dtype=dtype, device=dev)
+        y = u.new_empty(size)
     else:
-        _whole(y, "y", (b, T, Dc), dtype, dev)
-    shape = _selective_shape(b, T, Dc, G, N, *_strides(u), *_strides(dt), *(_strides(z) if z is not None else (0, 0)),
-                             *_strides(B), *_strides(C), _DT[dtype], _DT[dt.dtype], 1 if dt_softplus else 0, 0)
+        _whole(y, "y", size, dtype, u.device)
+    shape = _selective_shape(b, T, Dc, G, N, us[0], us[1], ds[0], ds[1], zs[0], zs[1], bs[0], bs[1], cs[0], cs[1],
+                             _DT[dtype], _DT[dt.dtype], 1 if dt_softplus else 0, 0)
     return N, shape, (u.data_ptr(), dt.data_ptr(), A.data_ptr(), B.data_ptr(), C.data_ptr(), _ptr(D),
                       _ptr(z), _ptr(dt_bias)), y
 
@@ -272,7 +310,7 @@ def _selective_states(u, nseq, N, initial_states, return_final_states, final_sta
     if final_states is not None:
         _whole(final_states, "final_states", size, torch.float32, u.device)
     elif return_final_states:
-        final_states = torch.empty(size, dtype=torch.float32, device=u.device)
+        final_states = u.new_empty(size, dtype=_F32)
     return final_states
 
 
@@ -290,7 +328,7 @@ def ssd_selective_scan(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     """
     N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
     fin = _selective_states(u, u.shape[0], N, initial_states, return_final_states, final_states)
-    _call("ssd_selective_scan", u.device, stream, shape, *ins, _ptr(initial_states), y.data_ptr(),
+    _call("ssd_selective_scan", u, stream, shape, *ins, _ptr(initial_states), y.data_ptr(),
           _ptr(fin))
     return (y, fin) if return_final_states else y
 
@@ -306,7 +344,7 @@ def ssd_selective_scan_varlen(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_s
     cu = _offsets(cu_seqlens, u.shape[1], u.device)
     n = cu.numel() - 1
     fin = _selective_states(u, n, N, initial_states, return_final_states, final_states)
-    _call("ssd_selective_scan_varlen", u.device, stream, shape, *ins, cu.data_ptr(), n,
+    _call("ssd_selective_scan_varlen", u, stream, shape, *ins, cu.data_ptr(), n,
           _ptr(initial_states), y.data_ptr(), _ptr(fin))
     return (y, fin) if return_final_states else y
 
@@ -322,5 +360,5 @@ def ssd_selective_step(u, dt, A, B, C, D, state, z=None, dt_bias=None, dt_softpl
         u, dt, B, C, z, y = (t.unsqueeze(1) if isinstance(t, torch.Tensor) else t for t in (u, dt, B, C, z, y))
     N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
     _whole(state, "state", (u.shape[0], u.shape[2], N), _F32, u.device)
-    _call("ssd_selective_step", u.device, stream, shape, *ins, state.data_ptr(), y.data_ptr())
+    _call("ssd_selective_step", u, stream, shape, *ins, state.data_ptr(), y.data_ptr())
     return y.squeeze(1) if one else y

@@ -129,7 +129,7 @@ ssd_status_t check_selective_shape(const ssd_selective_shape_t* s) {
     if (s->channels > kMaxRow) return SSD_ERR_UNSUPPORTED;
     for (const ssd_strides_t* p : {&s->u, &s->dt, &s->B, &s->C}) {
         if (!stride_ok(*p, s->batch, s->seqlen)) return SSD_ERR_INVALID_ARG;
-        if (p->row > kMaxRow) return SSD_ERR_UNSUPPORTED;
+        if (s->seqlen > 1 && p->row > kMaxRow) return SSD_ERR_UNSUPPORTED;
     }
     return SSD_OK;
 }
@@ -140,7 +140,7 @@ ssd_status_t check_selective(const ssd_selective_shape_t* s, int64_t nseq, const
                              const float* dt_bias, const int32_t* cu, const float* init, void* y, float* fin,
                              bool in_place, ssd::SelectiveArgs* a) {
     if (z && !stride_ok(s->z, s->batch, s->seqlen)) return SSD_ERR_INVALID_ARG;
-    if (z && s->z.row > kMaxRow) return SSD_ERR_UNSUPPORTED;
+    if (z && s->seqlen > 1 && s->z.row > kMaxRow) return SSD_ERR_UNSUPPORTED;
     const size_t es = elem_size(s->dtype), des = elem_size(s->dt_dtype);
     const int64_t b = s->batch, T = s->seqlen, Dc = s->channels, GN = s->ngroups * s->dstate;
     const size_t zu = span(s->u, b, T, Dc, es), zdt = span(s->dt, b, T, Dc, des);
