@@ -231,47 +231,54 @@ __global__ void __launch_bounds__(kRunWarps * 32, sizeof(E) == 2 ? 5 : 4) conv_k
             window[k] = widen(r);
         }
     };
-    open(t0);
     // Addresses are walked: a product of 64-bit strides for every row costs more than its arithmetic.
     const E* ut = u + t0 * p.ur;
     E* yt = out.y + t0 * out.stride;
     const int64_t ys = out.stride;
-    auto one = [&](E* to, const Vec<VW>& x) {
+    auto one = [&](const Vec<VW>& x) {
         Raw o;
         narrow(taps.template apply<kSilu>(window, x), o);
         push<W>(window, x);
-        __stcs(reinterpret_cast<Raw*>(to), o);
+        __stcs(reinterpret_cast<Raw*>(yt), o);
+        yt += ys;
     };
-    // Whole batches, the next one's loads in flight while this one is computed; the rest, and from
-    // the batch in which a document starts, token by token.
-    const int64_t whole = kPacked && next < t1 ? next : t1;
-    int left = (int)(whole > t0 ? whole - t0 : 0), tokens = (int)(t1 - t0);
     Raw raw[kBatch];
-    auto fetch = [&]() {
+    auto fetch = [&](int n) {                                // the next n <= kBatch tokens
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i, ut += p.ur) raw[i] = __ldcs(reinterpret_cast<const Raw*>(ut));
+        for (int i = 0; i < kBatch; ++i)
+            if (i < n) {
+                raw[i] = __ldcs(reinterpret_cast<const Raw*>(ut));
+                ut += p.ur;
+            }
     };
-    if (left >= kBatch) fetch();
-    for (; left >= kBatch; left -= kBatch, tokens -= kBatch) {
-        Vec<VW> x[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) x[i] = widen(raw[i]);
-        if (left >= 2 * kBatch) fetch();
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i, yt += ys) one(yt, x[i]);
-    }
-    for (int64_t t = t1 - tokens; t < t1; ++t, ut += p.ur, yt += ys) {
+    for (int64_t t = t0; t < t1;) {                          // the run's part of each document
         if constexpr (kPacked) {
-            if (t >= next && seq + 1 < p.nseq) {             // a document starts here: the last that does
+            if (t >= next && seq + 1 < p.nseq) {             // one starts here: the last that does
                 do {
                     ++seq;
                     next = p.cu[seq + 1];
                 } while (t >= next && seq + 1 < p.nseq);
                 start = t;
-                open(t);
             }
         }
-        one(yt, widen(*reinterpret_cast<const Raw*>(ut)));
+        const int64_t stop = kPacked && next > t && next < t1 ? next : t1;
+        int left = (int)(stop - t);
+        t = stop;
+        // whole batches, the next one's loads in flight while this one is computed
+        fetch(left);
+        open(t - left);
+        for (; left >= kBatch; left -= kBatch) {
+            Vec<VW> x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) x[i] = widen(raw[i]);
+            if (left >= 2 * kBatch) fetch(kBatch);
+            else fetch(left - kBatch);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) one(x[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch - 1; ++i)
+            if (i < left) one(widen(raw[i]));
     }
 }
 
@@ -340,7 +347,7 @@ cudaError_t conv_w(const ConvArgs& a, cudaStream_t st) {
     ConvParams p = params_of(a, VW);
     // Runs of 64 tokens read 5 % more rows than they write (L2 holds the halo); shorter ones where
     // there would be too few warps to keep the memory busy.
-    int run = 32;
+    int run = 64;
     while (run > kBatch && p.nvg * a.b * ((a.T + run - 1) / run) < 148 * 24) run /= 2;
     p.run = run;
     p.run_blocks = (a.T + (int64_t)run * kRunWarps - 1) / ((int64_t)run * kRunWarps);
