@@ -8,22 +8,16 @@
 //
 // What bounds it: one exponential for each (token, channel, state) on the special-function
 // unit, 16 a clock and SM (with 16 states: 16 + 4 for softplus and SiLU against 8 bytes of HBM
-// traffic in bf16, 3.6 times the time of the bytes), and beside it nearly as many issue slots.
-// So every exponential is computed once, also where the sequence is cut.
+// traffic in bf16, 3.6 times the time of the bytes), and beside it nearly as many issue slots:
+// four fp32 operations for each exponential, whose packed forms (fp32x2) take two slots each, and
+// what a (token, channel) needs once. So every exponential is computed once, also where a sequence
+// is cut, and what is left is moved off the inner loop.
 //
-// Layout: a warp takes 64 / SL channels, SL lanes for a pair of channels, 4 states a lane (more
-// than 4 SL states in blocks), and K tokens at a time. Its tokens' inputs arrive by asynchronous
-// copies a tile ahead; softplus and dt u are computed once per (token, channel); then each lane
-// runs its 2 x 4 states through the tokens with packed fp32x2 arithmetic. Two channels a lane
-// halve the reads of B and C from shared memory, whose port otherwise binds before the
-// exponentials. The lanes' parts of y are summed by exchanges that leave every lane K / SL tokens.
-//
-// The cut (kSplit): where there are few channels, the warps of a CTA take consecutive runs of K
-// tokens of the same channels. Each runs from a state of zero and keeps, per token and state, C_t
-// times the product of its decays so far. The entering states go from warp to warp as a chain,
-// h <- (prod a) h + h_local, over shared memory and a named barrier of the two warps, so that the
-// warps stay at different phases; with its entering state a warp adds sum_n (C_t prod a)[n] h[n]
-// to each y_t, at two packed operations per pair of states and no second exponential.
+// Two forms, both with their inputs copied asynchronously a tile ahead:
+//   many channels (wide_scan_kernel): a lane holds the states of a channel, nothing is exchanged
+//     between lanes, and two warps take the tiles of a block of channels in turn;
+//   few channels (cut_scan_kernel): four lanes share a pair of channels, and the warps of a CTA take
+//     consecutive runs of tokens of the same channels.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -116,18 +110,6 @@ __device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, i
     }
 }
 
-// A warp's shared memory: two stages of inputs, and the tile's (dt, dt u).
-template <typename E, typename Td, int SL, int K>
-struct WarpMem {
-    static constexpr int CH = 64 / SL, NS = 4 * SL;
-    alignas(16) E u[2][K][CH];
-    alignas(16) E z[2][K][CH];
-    alignas(16) Td dt[2][K][CH];
-    alignas(16) E B[2][K][NS];
-    alignas(16) E C[2][K][NS];
-    alignas(16) float4 s[K][CH / 2];          // dt, dt u of two channels
-};
-
 // Two neighbouring elements.
 __device__ __forceinline__ float2 pair_of(const float* p) { return *reinterpret_cast<const float2*>(p); }
 __device__ __forceinline__ float2 pair_of(const __nv_bfloat16* p) {
@@ -139,16 +121,277 @@ __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float2 v) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16(v.x, v.y);
 }
 // Four neighbouring elements as two pairs.
-__device__ __forceinline__ void quad_of(const float* p, float2 (&v)[2]) {
+__device__ __forceinline__ void quad_of(const float* p, float2* v) {
     const float4 q = *reinterpret_cast<const float4*>(p);
     v[0] = make_float2(q.x, q.y);
     v[1] = make_float2(q.z, q.w);
 }
-__device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2 (&v)[2]) {
+__device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2* v) {
     const uint2 q = *reinterpret_cast<const uint2*>(p);
     v[0] = make_float2(bf16_lo(q.x), bf16_hi(q.x));
     v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
 }
+
+// ---- many channels -----------------------------------------------------------
+//
+// A lane holds a channel's states (16 at a time), so that softplus, dt u, the gate and y stay in the
+// lane, and B and C are read by all lanes at one address (half the time of distinct ones). The two
+// warps of a CTA take the tiles of 32 channels in turn and hand the states over through shared
+// memory: while one runs the states through its tile, the other computes the steps of its next and
+// finishes its last. Against four lanes a pair of channels (4 x 2048 tokens of 5120 channels): 16
+// states in fp32 377 us for 459, 8 states in bf16 224 for 304, 16 states in bf16 353 for 349.
+constexpr int kWideTok = 16, kWideWarps = 2;
+
+template <typename E, typename Td, int NS>
+struct WideMem {
+    alignas(16) E u[2][kWideTok][32];
+    alignas(16) E z[2][kWideTok][32];
+    alignas(16) Td dt[2][kWideTok][32];
+    alignas(16) E B[2][kWideTok][NS];
+    alignas(16) E C[2][kWideTok][NS];
+    alignas(16) float Bf[sizeof(E) == 2 ? kWideTok : 1][NS];
+    alignas(16) float Cf[sizeof(E) == 2 ? kWideTok : 1][NS];
+};
+template <int K, int NS>
+__device__ __forceinline__ void widen(float (*dst)[NS], const __nv_bfloat16 (*src)[NS], int lane) {
+#pragma unroll
+    for (int i = 0; i < (K * NS + 127) / 128; ++i) {
+        const int at = (lane + 32 * i) * 4;
+        if (K * NS % 128 == 0 || at < K * NS) {
+            float2 v[2];
+            quad_of(&src[0][0] + at, v);
+            *reinterpret_cast<float4*>(&dst[0][0] + at) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        }
+    }
+}
+template <typename E>
+__device__ __forceinline__ float2 tokens_of(const E (*rows)[32], int k, int lane) {    // of tokens k and k + 1
+    return make_float2(to_float(rows[k][lane]), to_float(rows[k + 1][lane]));
+}
+
+// kBlocks: more states than NS, which the inner loops then take a block at a time
+template <typename E, typename Td, int NS, bool kBlocks>
+__global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __grid_constant__ ScanParams p) {
+    constexpr int K = kWideTok, P = NS / 2, W = kWideWarps;
+    using Mem = WideMem<E, Td, NS>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const SelectiveArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int NB = kBlocks ? p.nblocks : 1;
+    Mem& m = reinterpret_cast<Mem*>(smem)[warp];
+    // by state block: the states entering the next tile, and (with several blocks) the rates
+    float2* const carry = reinterpret_cast<float2*>(smem + W * sizeof(Mem)) + lane;     // [NB][P][32]
+    float2* const rates = carry + NB * P * 32;
+    const int64_t unit = blockIdx.x, per_seq = p.cblocks * a.G;
+    const int64_t seq = unit / per_seq, g = unit % per_seq / p.cblocks, c0 = unit % p.cblocks * 32;
+    const int64_t b = a.cu ? 0 : seq;
+    int t0 = 0, t1 = (int)a.T;
+    if (a.cu) {
+        t0 = min(max(a.cu[seq], 0), t1);
+        t1 = min(max(a.cu[seq + 1], 0), t1);
+    }
+    const int cols = (int)min(p.per - c0, (int64_t)32);
+    const int64_t d0 = g * p.per + c0;
+    const int N = (int)a.N;
+    const bool in = lane < cols;
+    const int64_t d = d0 + (in ? lane : 0);
+    const float2 skip = both(a.Dskip ? a.Dskip[d] : 0.f), bias = both(a.dt_bias ? a.dt_bias[d] : 0.f);
+    float2 A[P];
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            float v[2], r[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int n = nb * NS + 2 * i + x;
+                v[x] = a.init && n < N ? a.init[(seq * a.D + d) * N + n] : 0.f;
+                r[x] = n < N ? a.A[d * N + n] * kLog2e : 0.f;
+            }
+            A[i] = make_float2(r[0], r[1]);
+            if (warp == 0) {
+                carry[(nb * P + i) * 32] = make_float2(v[0], v[1]);
+                if (NB > 1) rates[(nb * P + i) * 32] = A[i];
+            }
+        }
+    }
+    if (NB > 1) __syncthreads();
+    const E* const ub = static_cast<const E*>(a.u) + b * a.us.batch + d0;
+    const Td* const dtb = static_cast<const Td*>(a.dt) + b * a.dts.batch + d0;
+    const E* const zb = a.z ? static_cast<const E*>(a.z) + b * a.zs.batch + d0 : nullptr;
+    const E* const Bb = static_cast<const E*>(a.B) + b * a.Bs.batch + g * N;
+    const E* const Cb = static_cast<const E*>(a.C) + b * a.Cs.batch + g * N;
+    const int ur = (int)a.us.row, dtr = (int)a.dts.row, zr = (int)a.zs.row, Br = (int)a.Bs.row, Cr = (int)a.Cs.row;
+    // the copies of the tile at token t, state block nb; u, dt, z (stage sr) with the first block
+    auto issue = [&](int t, int nb, int sr, int sb) {
+        const int n = min(t1 - t, K);
+        if (n > 0) {
+            if (nb == 0) {
+                stage<K, 32>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
+                stage<K, 32>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
+                if (zb) stage<K, 32>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
+            }
+            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc16);
+        }
+        copy_commit();
+    };
+    const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
+    E* const yb = static_cast<E*>(a.y) + b * a.T * a.D + d0 + lane;
+    int t = t0 + warp * K, sr = 0, sb = 0;
+    issue(t, 0, 0, 0);
+    for (int it = warp; it < tiles; it += W, t += W * K, sr ^= 1) {
+        const int n = min(t1 - t, K);
+        float2 dt[K / 2], du[K / 2], yv[K / 2];              // of two tokens each
+        for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
+            __syncwarp();                                    // the stage that is filled next has been read
+            if (nb + 1 < NB) issue(t, nb + 1, sr ^ 1, sb ^ 1);
+            else issue(t + W * K, 0, sr ^ 1, sb ^ 1);
+            copy_wait<1>();
+            __syncwarp();
+            if (nb == 0) {
+                // past the end the step and dt u are 0, which leaves the state as it is
+#pragma unroll
+                for (int q = 0; q < K / 2; ++q) dt[q] = add_(tokens_of(m.dt[sr], 2 * q, lane), bias);
+                if (a.softplus) {
+#pragma unroll
+                    for (int q = 0; q < K / 2; ++q) dt[q] = softplus(dt[q]);
+                }
+                if (n < K) {
+#pragma unroll
+                    for (int q = 0; q < K / 2; ++q)
+                        dt[q] = make_float2(2 * q < n ? dt[q].x : 0.f, 2 * q + 1 < n ? dt[q].y : 0.f);
+                }
+#pragma unroll
+                for (int q = 0; q < K / 2; ++q) {
+                    du[q] = mul_(dt[q], tokens_of(m.u[sr], 2 * q, lane));
+                    if (kBlocks) yv[q] = both(0.f);
+                }
+            }
+            const float* Bt;
+            const float* Ct;
+            if constexpr (sizeof(E) == 2) {
+                widen<K, NS>(m.Bf, m.B[sb], lane);
+                widen<K, NS>(m.Cf, m.C[sb], lane);
+                __syncwarp();
+                Bt = &m.Bf[0][0];
+                Ct = &m.Cf[0][0];
+            } else {
+                Bt = &m.B[sb][0][0];
+                Ct = &m.C[sb][0][0];
+            }
+            // barrier w: the other warp has run its tile, whose states are in carry
+            if (nb == 0 && it > 0) pair_wait<W>(warp);
+            float2 h[P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                h[i] = carry[(nb * P + i) * 32];
+                if (NB > 1) A[i] = rates[(nb * P + i) * 32];
+            }
+            // a token's decays, B and C while the states of the one before are computed
+            float2 e[2][P], Bv[2][P], Cv[2][P];
+            auto prepare = [&](int k) {
+                const float st = k % 2 ? dt[k / 2].y : dt[k / 2].x;
+#pragma unroll
+                for (int i = 0; i < P; i += 2) {
+                    quad_of(Bt + k * NS + 2 * i, Bv[k & 1] + i);
+                    quad_of(Ct + k * NS + 2 * i, Cv[k & 1] + i);
+                }
+#pragma unroll
+                for (int i = 0; i < P; ++i) e[k & 1][i] = ex2(mul_(both(st), A[i]));
+            };
+            prepare(0);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const float su = k % 2 ? du[k / 2].y : du[k / 2].x;
+                if (k + 1 < K) prepare(k + 1);
+                float2 r[2] = {both(0.f), both(0.f)};
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    h[i] = fma_(e[k & 1][i], h[i], mul_(both(su), Bv[k & 1][i]));
+                    r[i & 1] = fma_(Cv[k & 1][i], h[i], r[i & 1]);
+                }
+                r[0] = add_(r[0], r[1]);
+                float& y = k % 2 ? yv[k / 2].y : yv[k / 2].x;
+                y = kBlocks ? y + (r[0].x + r[0].y) : r[0].x + r[0].y;
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) carry[(nb * P + i) * 32] = h[i];
+        }
+        if (it + 1 < tiles) pair_arrive<W>(warp ^ 1);
+#pragma unroll
+        for (int q = 0; q < K / 2; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * q, lane), yv[q]);
+        if (zb) {
+#pragma unroll
+            for (int q = 0; q < K / 2; ++q) yv[q] = mul_(yv[q], silu(tokens_of(m.z[sr], 2 * q, lane)));
+        }
+        E* to = yb + (int64_t)t * (int)a.D;
+        if (n == K && cols == 32) {
+#pragma unroll
+            for (int q = 0; q < K / 2; ++q, to += 2 * a.D) {
+                store_elem(to, yv[q].x);
+                store_elem(to + a.D, yv[q].y);
+            }
+        } else if (in) {
+#pragma unroll
+            for (int q = 0; q < K / 2; ++q, to += 2 * a.D) {
+                if (2 * q < n) store_elem(to, yv[q].x);
+                if (2 * q + 1 < n) store_elem(to + a.D, yv[q].y);
+            }
+        }
+    }
+    copy_wait<0>();
+    // the warp that wrote the carried states last
+    if (!a.fin || !in || warp != (tiles == 0 ? 0 : (tiles - 1) % W)) return;
+    for (int n = 0; n < N; ++n) {
+        const float2 h = carry[n / 2 * 32];
+        a.fin[(seq * a.D + d) * N + n] = n % 2 ? h.y : h.x;
+    }
+}
+
+template <typename E, typename Td, int NS, bool kBlocks>
+cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
+    const SelectiveArgs& a = p.a;
+    p.cblocks = (p.per + 31) / 32;
+    p.nblocks = (int)((a.N + NS - 1) / NS);
+    const int64_t units = a.nseq * a.G * p.cblocks;
+    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const size_t shared = kWideWarps * sizeof(WideMem<E, Td, NS>) + (size_t)p.nblocks * NS * 32 * 4 * (p.nblocks > 1 ? 2 : 1);
+    auto kernel = wide_scan_kernel<E, Td, NS, kBlocks>;
+    if (shared > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<(unsigned)units, kWideWarps * 32, shared, st>>>(p);
+    return cudaGetLastError();
+}
+
+// ---- few channels ------------------------------------------------------------
+//
+// A warp takes 64 / SL channels, SL lanes for a pair of channels, 4 states a lane (more than 4 SL
+// states in blocks), and kCutTok tokens at a time: softplus and dt u are computed once per (token,
+// channel) and shared through shared memory, each lane runs its 2 x 4 states through the tokens (two
+// channels a lane halve the reads of B and C), and the lanes' parts of y are summed by exchanges that
+// leave every lane kCutTok / SL tokens.
+//
+// The W warps of a CTA take consecutive runs of kCutTok tokens of the same channels. Each runs from a
+// state of zero and keeps, per token and state, C_t times the product of its decays so far. The
+// entering states go from warp to warp as a chain, h <- (prod a) h + h_local, over shared memory and
+// a named barrier of the two warps, so that the warps stay at different phases; with its entering
+// state a warp adds sum_n (C_t prod a)[n] h[n] to each y_t, at two packed operations per pair of
+// states and no second exponential. 16384 tokens of 2048 channels, 16 states, fp32: 8 warps 526 us,
+// 16 warps 379 (no cut: 1308).
+constexpr int kCutTok = 8;       // 8 floats a token and lane are kept
+
+template <typename E, typename Td, int SL>
+struct CutMem {
+    static constexpr int CH = 64 / SL, NS = 4 * SL;
+    alignas(16) E u[2][kCutTok][CH];
+    alignas(16) E z[2][kCutTok][CH];
+    alignas(16) Td dt[2][kCutTok][CH];
+    alignas(16) E B[2][kCutTok][NS];
+    alignas(16) E C[2][kCutTok][NS];
+    alignas(16) float4 s[kCutTok][CH / 2];    // dt, dt u of two channels
+};
 
 // 2 x 4 states of a lane (or their decays): [channel of the pair][pair of states]
 struct States {
@@ -167,31 +410,19 @@ struct States {
     }
 };
 
-// Forms of the kernel. kAlternate: the two warps of a CTA take the tiles of one unit (sequence, block
-// of channels) in turn, and while one runs the states through its tile the other prepares its next
-// and finishes its last. kCut4, 8, 16: the cut form with that many warps.
-enum Form { kAlternate = 2, kCut4 = 4, kCut8 = 8, kCut16 = 16 };
-__host__ __device__ constexpr int form_warps(Form f) { return (int)f; }
-// resident CTAs per SM that the registers are capped for
-__host__ __device__ constexpr int form_ctas(Form f) { return f == kAlternate ? 9 : 16 / (int)f; }
-// tokens of a warp's tile: the cut form keeps 8 floats a token in registers, and with few states a
-// lane's rows are wide
-__host__ __device__ constexpr int form_tokens(Form f, int SL) { return f != kAlternate || SL < 4 ? 8 : 16; }
-
-template <typename E, typename Td, int SL, Form F>
-__global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(const __grid_constant__ ScanParams p) {
-    constexpr bool kCut = F != kAlternate;
-    constexpr int W = form_warps(F), K = form_tokens(F, SL);
+template <typename E, typename Td, int SL, int W>
+__global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_constant__ ScanParams p) {
+    constexpr int K = kCutTok;
     constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
-    using Mem = WarpMem<E, Td, SL, K>;
+    using Mem = CutMem<E, Td, SL>;
     extern __shared__ __align__(16) unsigned char smem[];
     const SelectiveArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int cp = lane % CL, j = lane / CL;             // pair of channels, states 4 j ..
     const int NB = p.nblocks;
     Mem& m = reinterpret_cast<Mem*>(smem)[warp];
-    // the states entering the next tile (cut: the next W tiles), by state block; cut: two slots a warp
-    // for what its predecessor hands over
+    // the states entering the next round of W tiles, by state block; two slots a warp for what its
+    // predecessor hands over
     float4* const carry = reinterpret_cast<float4*>(smem + W * sizeof(Mem));
     float4* const slots = carry + NB * 64;
 
@@ -254,20 +485,16 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
 
     E* const yb = static_cast<E*>(a.y) + b * a.T * a.D + d0 + 2 * cp;
     const int64_t Dr = a.D;
-    // Cut: all warps take part in every round of W tiles, those past the end too, which pass the
-    // states on. Alternating: a warp takes every second tile.
-    const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
-    const int rounds = (tiles + W - 1) / W;
-    const int mine = kCut ? rounds : (tiles - warp + W - 1) / W;
+    // all warps take part in every round of W tiles, those past the end too, which pass the states on
+    const int rounds = t1 > t0 ? (t1 - t0 + W * K - 1) / (W * K) : 0;
     // y of a pair of channels: the lane's parts, and, summed over the SL lanes that share the pair by
     // exchanges of SL tokens each, the tokens q SL + j that the lane finishes
-    constexpr int kHeld = kCut ? K : SL;
-    float2 yv[kHeld], ysum[K / SL] = {};
+    float2 yv[K], ysum[K / SL] = {};
     auto give = [&](float2 v, int mask) {
         return make_float2(__shfl_xor_sync(0xffffffffu, v.x, mask), __shfl_xor_sync(0xffffffffu, v.y, mask));
     };
     auto gather = [&](int q) {
-        const float2* const v = yv + q * SL % kHeld;
+        const float2* const v = yv + q * SL;
         float2 r;
         if constexpr (SL == 4) {
             const bool up = j & 2, odd = j & 1;
@@ -289,14 +516,14 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
     };
     if (NB == 1) rates(0);
     int t = t0 + warp * K, sr = 0, sb = 0;
-    if (mine > 0) issue(t, 0, 0, 0);
-    for (int it = 0; it < mine; ++it, t += W * K, sr ^= 1) {
+    if (rounds > 0) issue(t, 0, 0, 0);
+    for (int it = 0; it < rounds; ++it, t += W * K, sr ^= 1) {
         const int n = min(t1 - t, K);
         for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
             __syncwarp();                                // the stage that is filled next has been read
             if (nb + 1 < NB)
                 issue(t, nb + 1, sr ^ 1, sb ^ 1);
-            else if (it + 1 < mine)
+            else if (it + 1 < rounds)
                 issue(t + W * K, 0, sr ^ 1, sb ^ 1);
             else
                 copy_commit();
@@ -331,15 +558,9 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
                 for (int q = 0; q < K / SL; ++q) ysum[q] = both(0.f);
             }
             States h, decay;
-            float2 gc[kCut ? K : 1][2][2];               // C_t times the decays up to t
+            float2 gc[K][2][2];               // C_t times the decays up to t
             decay.fill(1.f);
-            if constexpr (kCut) {
-                h.fill(0.f);
-            } else {
-                // barrier w: the other warp has run its tile, whose states are in carry
-                if (nb == 0 && (it > 0 || warp > 0)) pair_wait<W>(warp);
-                h.load(carry + nb * 64 + lane);
-            }
+            h.fill(0.f);
             if (n > 0) {
                 const E* const Bt = &m.B[sb][0][0] + j * 4;
                 const E* const Ct = &m.C[sb][0][0] + j * 4;
@@ -373,60 +594,52 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
                             const float2 ek = e[k & 1][c][i];
                             h.v[c][i] = fma_(ek, h.v[c][i], mul_(du, Bv[i]));
                             r = i ? fma_(Cv[i], h.v[c][i], r) : mul_(Cv[i], h.v[c][i]);
-                            if constexpr (kCut) {
-                                decay.v[c][i] = k ? mul_(decay.v[c][i], ek) : ek;
-                                gc[k][c][i] = mul_(Cv[i], decay.v[c][i]);
-                            }
+                            decay.v[c][i] = k ? mul_(decay.v[c][i], ek) : ek;
+                            gc[k][c][i] = mul_(Cv[i], decay.v[c][i]);
                         }
                         part[c] = r.x + r.y;
                     }
-                    yv[k % kHeld] = make_float2(part[0], part[1]);
-                    if (!kCut && k % SL == SL - 1) gather(k / SL);
+                    yv[k] = make_float2(part[0], part[1]);
                 }
             }
-            if constexpr (kCut) {
-                // The entering state: the first warp's is what the last one left of the round before,
-                // any other's comes from its predecessor (barrier w, and slot w by parity). The first
-                // warp is told once a round. With one state block a predecessor cannot come to its
-                // next hand-over before this one has gone round the chain, and need not wait; with
-                // several, both wait, and the second slot keeps the next hand-over off this one.
-                float4* const slot = slots + (((it * NB + nb) & 1) * W + warp) * 64 + lane;
-                if (warp == 0) {
-                    if (it > 0 && nb == 0) pair_wait<W>(0);
-                } else {
-                    pair_wait<W>(warp);
-                }
-                States in;
-                in.load(warp == 0 ? carry + nb * 64 + lane : slot);
+            // The entering state: the first warp's is what the last one left of the round before,
+            // any other's comes from its predecessor (barrier w, and slot w by parity). The first
+            // warp is told once a round. With one state block a predecessor cannot come to its
+            // next hand-over before this one has gone round the chain, and need not wait; with
+            // several, both wait, and the second slot keeps the next hand-over off this one.
+            float4* const slot = slots + (((it * NB + nb) & 1) * W + warp) * 64 + lane;
+            if (warp == 0) {
+                if (it > 0 && nb == 0) pair_wait<W>(0);
+            } else {
+                pair_wait<W>(warp);
+            }
+            States in;
+            in.load(warp == 0 ? carry + nb * 64 + lane : slot);
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) h.v[c][i] = fma_(decay.v[c][i], in.v[c][i], h.v[c][i]);
-                if (warp + 1 < W) {
-                    h.store(slot + 64);
-                    if (NB == 1) pair_arrive<W>(warp + 1);
-                    else pair_wait<W>(warp + 1);
-                } else {
-                    h.store(carry + nb * 64 + lane);
-                    if (nb == NB - 1 && it + 1 < mine) pair_arrive<W>(0);
-                }
-                if (n > 0) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        float part[2];
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float2 r =
-                                fma_(gc[k][c][1], in.v[c][1], mul_(gc[k][c][0], in.v[c][0]));
-                            part[c] = r.x + r.y;
-                        }
-                        yv[k % kHeld] = add_(yv[k % kHeld], make_float2(part[0], part[1]));
-                        if (k % SL == SL - 1) gather(k / SL);
-                    }
-                }
+                for (int i = 0; i < 2; ++i) h.v[c][i] = fma_(decay.v[c][i], in.v[c][i], h.v[c][i]);
+            if (warp + 1 < W) {
+                h.store(slot + 64);
+                if (NB == 1) pair_arrive<W>(warp + 1);
+                else pair_wait<W>(warp + 1);
             } else {
                 h.store(carry + nb * 64 + lane);
-                if (nb == NB - 1 && t + K < t1) pair_arrive<W>(warp ^ 1);
+                if (nb == NB - 1 && it + 1 < rounds) pair_arrive<W>(0);
+            }
+            if (n > 0) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    float part[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float2 r =
+                            fma_(gc[k][c][1], in.v[c][1], mul_(gc[k][c][0], in.v[c][0]));
+                        part[c] = r.x + r.y;
+                    }
+                    yv[k] = add_(yv[k], make_float2(part[0], part[1]));
+                    if (k % SL == SL - 1) gather(k / SL);
+                }
             }
         }
         if (n <= 0) continue;
@@ -452,7 +665,7 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
     }
     copy_wait<0>();
     // the warp that wrote the carried states last
-    if (!a.fin || warp != (tiles == 0 ? 0 : kCut ? W - 1 : (tiles - 1) % W)) return;
+    if (!a.fin || warp != (rounds == 0 ? 0 : W - 1)) return;
     for (int nb = 0; nb < NB; ++nb) {
         States h;
         h.load(carry + nb * 64 + lane);
@@ -468,12 +681,10 @@ __global__ void __launch_bounds__(form_warps(F) * 32, form_ctas(F)) scan_kernel(
     }
 }
 
-template <typename E, typename Td, int SL, Form F>
-cudaError_t launch_form(const ScanParams& p, int64_t units, cudaStream_t st) {
-    constexpr int W = form_warps(F);
-    const size_t shared = W * sizeof(WarpMem<E, Td, SL, form_tokens(F, SL)>) +
-                          (size_t)(p.nblocks + (F == kAlternate ? 0 : 2 * W)) * 64 * 16;
-    auto kernel = scan_kernel<E, Td, SL, F>;
+template <typename E, typename Td, int SL, int W>
+cudaError_t launch_cut(const ScanParams& p, int64_t units, cudaStream_t st) {
+    const size_t shared = W * sizeof(CutMem<E, Td, SL>) + (size_t)(p.nblocks + 2 * W) * 64 * 16;
+    auto kernel = cut_scan_kernel<E, Td, SL, W>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
@@ -486,19 +697,23 @@ template <typename E, typename Td, int SL>
 cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
     constexpr int CH = 64 / SL, NS = 4 * SL;
     const SelectiveArgs& a = p.a;
-    p.cblocks = (p.per + CH - 1) / CH;
-    p.nblocks = (int)((a.N + NS - 1) / NS);
-    const int64_t units = a.nseq * a.G * p.cblocks;
-    if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const int64_t cblocks = (p.per + CH - 1) / CH, units = a.nseq * a.G * cblocks;
     const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
-    // The cut form where the channels alone leave the SMs with few warps: as many warps a unit as
-    // keep an SM at 16 (a tile's K tokens each, so no more than the sequence fills).
-    constexpr bool kFits16 = 16 * sizeof(WarpMem<E, Td, SL, form_tokens(kCut16, SL)>) <= 160 * 1024;
-    if (units >= 4 * 148 || len <= 32) return launch_form<E, Td, SL, kAlternate>(p, units, st);
-    if (units > 2 * 148 || len <= 64) return launch_form<E, Td, SL, kCut4>(p, units, st);
-    if constexpr (kFits16)
-        if (units <= 148 && len > 128) return launch_form<E, Td, SL, kCut16>(p, units, st);
-    return launch_form<E, Td, SL, kCut8>(p, units, st);
+    // One wave of CTAs is the cut form's (one of 16 warps or two of 8 on each SM): beyond it, and for
+    // short sequences, the uncut form (2048 tokens, 16 states, bf16: 4096 channels 106 us cut, 171
+    // uncut; 8192 channels 207 cut, 175 uncut).
+    if (units > 2 * 148 || len <= 8 * kCutTok) {
+        if constexpr (SL == 4)
+            if (a.N > NS) return launch_wide<E, Td, NS, true>(p, st);
+        return launch_wide<E, Td, NS, false>(p, st);
+    }
+    p.cblocks = cblocks;
+    p.nblocks = (int)((a.N + NS - 1) / NS);
+    // 16 warps where the shared memory of one CTA has room for them
+    constexpr bool kFits = 16 * sizeof(CutMem<E, Td, SL>) <= 160 * 1024;
+    if constexpr (kFits)
+        if (units <= 148 && len > 128) return launch_cut<E, Td, SL, 16>(p, units, st);
+    return launch_cut<E, Td, SL, 8>(p, units, st);
 }
 
 template <typename E, typename Td>
