@@ -136,6 +136,25 @@ def test_conv_packed(ssd, cu, dtype, C):
             assert np.array_equal(fin.double().cpu().numpy(), f)
 
 
+@pytest.mark.parametrize("C,dtype", [(8192, "bf16"), (2047, "f32")])
+def test_conv_long_runs(ssd, C, dtype):
+    """Enough rows for runs of 64 tokens a warp: a batch, and a pack whose documents start and end
+    everywhere in them, one after another, empty and single ones among them."""
+    cu = [0, 3, 64, 64, 65, 130, 191, 193, 700, 1024, 1087, 1088, 1100, 2500, 4101]
+    T = cu[-1] if C > 4096 else 16 * cu[-1]
+    cu = [c * T // cu[-1] for c in cu]
+    d = inputs(1, T, C, 4, dtype, nseq=len(cu) - 1, seed=1)
+    ref, bound, f = reference(d, True, cu)
+    y, fin = ssd.ssd_causal_conv1d_varlen(**cuda(d), cu_seqlens=cu, return_final_states=True)
+    check(y, ref, bound, dtype)
+    assert np.array_equal(fin.double().cpu().numpy(), f)
+    d["initial_states"] = d["initial_states"][:1]
+    whole = ssd.ssd_causal_conv1d(**cuda(d))
+    # a document's tokens past its first three see no boundary
+    for p, q in zip(cu, cu[1:]):
+        assert torch.equal(whole[:, p + 3:q], y[:, p + 3:q])
+
+
 def test_conv_rows_behind_the_last_document_stay(ssd):
     d = inputs(1, 200, 64, 4, "bf16", nseq=3, seed=5)
     cu = [0, 40, 41, 131]

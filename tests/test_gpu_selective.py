@@ -144,6 +144,23 @@ def test_scan_shapes(ssd, b, T, D, G, N, dtype, dt):
     run_and_check(ssd, inputs(b, T, D, G, N, dtype, dt, seed=T + N))
 
 
+@pytest.mark.parametrize("b,T,D,G,N,dtype", [
+    # many channels: a lane each, two warps in turn; over one, two and several tiles of 16 tokens
+    (1, 16, 4800, 1, 16, "bf16"), (2, 70, 4801, 1, 16, "f32"), (3, 33, 9600, 2, 8, "bf16"),
+    (1, 65, 19300, 1, 4, "f32"), (2, 17, 9664, 1, 3, "bf16"), (1, 50, 4800, 150, 13, "bf16"),
+    # many channels and more states than a lane holds at once
+    (4, 140, 4800, 1, 17, "bf16"), (8, 131, 2400, 1, 35, "f32"),
+    # few channels: 8 and 16 warps, several rounds, states in blocks and not
+    (2, 200, 2400, 1, 20, "bf16"), (1, 200, 2416, 1, 16, "f32"), (1, 300, 40, 1, 64, "bf16"),
+    (1, 290, 20, 2, 130, "f32"), (1, 400, 33, 1, 7, "bf16"), (1, 200, 70, 1, 2, "f32"),
+    # few channels, few tokens
+    (1, 5, 40, 1, 40, "bf16"), (1, 64, 16, 1, 16, "f32"), (1, 63, 16, 1, 17, "f32"),
+])
+def test_scan_forms(ssd, b, T, D, G, N, dtype):
+    """Sizes on both sides of every choice between the kernels' forms."""
+    run_and_check(ssd, inputs(b, T, D, G, N, dtype, seed=N))
+
+
 @pytest.mark.parametrize("softplus", [True, False])
 @pytest.mark.parametrize("gate", [True, False])
 @pytest.mark.parametrize("skip,states", [(True, False), (False, True)])
@@ -225,6 +242,17 @@ def test_scan_packed(ssd, cu, dtype, D, N):
             check(fin, rh, hb, torch.float32)
 
 
+def test_scan_packed_many_channels(ssd):
+    """Documents of every length around a tile, many of them, in the form for many channels."""
+    cu = [0, 1, 1, 17, 33, 48, 49, 81, 112, 113, 145, 177, 178]
+    for dtype, N in (("bf16", 16), ("f32", 20)):
+        d = inputs(1, cu[-1], 1600 if N == 16 else 1700, 1, N, dtype, nseq=len(cu) - 1, seed=N)
+        ry, yb, rh, hb = reference(d, cu)
+        y, fin = ssd.ssd_selective_scan_varlen(**cuda(d), cu_seqlens=cu, return_final_states=True)
+        check(y, ry, yb, d["u"].dtype)
+        check(fin, rh, hb, torch.float32)
+
+
 def test_scan_rows_behind_the_last_document_stay(ssd):
     d = inputs(1, 200, 32, 1, 16, "bf16", nseq=3, seed=5)
     cu = [0, 40, 41, 131]
@@ -263,6 +291,47 @@ def test_step(ssd, b, T, D, G, N, dtype, dt):
         y = ssd.ssd_selective_step(**dev, state=state)
         check(y, ry, yb, d["u"].dtype)
         check(state, rh, hb, torch.float32)
+
+
+@pytest.mark.parametrize("b,D,N,dtype", [
+    # several batch rows a thread, the last ones short: 4, 2 and 1 lanes a channel, one state at a
+    # time, several pieces a lane
+    (17, 4800, 16, "bf16"), (18, 4797, 16, "f32"), (17, 10000, 8, "bf16"), (19, 20000, 4, "f32"),
+    (17, 2403, 5, "bf16"), (17, 10000, 2, "f32"), (18, 20000, 1, "bf16"), (17, 1300, 48, "f32"),
+    (13, 400, 256, "bf16"), (17, 600, 50, "f32"), (17, 600, 99, "bf16"), (13, 404, 255, "f32"),
+])
+def test_step_many_rows(ssd, b, D, N, dtype):
+    d = inputs(b, 2, D, 1, N, dtype, seed=N)
+    ry, yb, rh, hb = reference(d)
+    dev = cuda(d)
+    state = dev.pop("initial_states")
+    y = ssd.ssd_selective_step(**dev, state=state)
+    check(y, ry, yb, d["u"].dtype)
+    check(state, rh, hb, torch.float32)
+
+
+def test_step_from_an_unaligned_state(ssd):
+    """States, A, B and C that start on 4 (2) bytes only."""
+    for dtype in ("f32", "bf16"):
+        d = inputs(3, 2, 24, 1, 16, dtype, seed=3)
+        ry, yb, rh, hb = reference(d)
+        dev = cuda(d)
+
+        def moved(t):
+            flat = torch.zeros(t.numel() + 1, dtype=t.dtype, device="cuda")
+            flat[1:] = t.reshape(-1)
+            return flat[1:].view(t.shape)
+        state = moved(dev.pop("initial_states"))
+        for k in ("A", "B", "C", "u", "dt", "z"):
+            dev[k] = moved(dev[k])
+        init = state.clone()
+        y = ssd.ssd_selective_step(**dev, state=state)
+        check(y, ry, yb, d["u"].dtype)
+        check(state, rh, hb, torch.float32)
+        y, fin = ssd.ssd_selective_scan(**dev, initial_states=moved(init), return_final_states=True,
+                                        y=moved(torch.zeros_like(y)))
+        check(y, ry, yb, d["u"].dtype)
+        check(fin, rh, hb, torch.float32)
 
 
 def test_step_one_token_form_and_slices(ssd):
