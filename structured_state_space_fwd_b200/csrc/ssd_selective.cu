@@ -134,19 +134,22 @@ __device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2* v) {
 
 // ---- many channels -----------------------------------------------------------
 //
-// A lane holds a channel's states (16 at a time), so that softplus, dt u, the gate and y stay in the
-// lane, and B and C are read by all lanes at one address (half the time of distinct ones). The two
-// warps of a CTA take the tiles of 32 channels in turn and hand the states over through shared
-// memory: while one runs the states through its tile, the other computes the steps of its next and
-// finishes its last. Against four lanes a pair of channels (4 x 2048 tokens of 5120 channels): 16
-// states in fp32 377 us for 459, 8 states in bf16 224 for 304, 16 states in bf16 353 for 349.
+// S = 2 lanes (1 with up to 4 states) hold a channel's states, 8 each of 16 at a time, and every
+// second pair of its tokens' steps, gates and outputs; B and C are read at one address by each half of
+// the warp, in less time than distinct ones. The two warps of a CTA take the tiles of 32 / S channels in
+// turn and hand the states over through shared memory: while one runs the states through its tile,
+// the other computes the steps of its next and finishes its last. 168 registers, which keep the next
+// token's decays, B and C in flight, are worth more than twice the warps (4 x 2048 tokens of 5120
+// channels, 16 states, bf16: 320 us with 6 CTAs an SM, 345 with 8, 338 with 9, 336 with 11; one lane a
+// channel 353; four lanes for a pair of channels 349), except where states come in blocks.
 constexpr int kWideTok = 16, kWideWarps = 2;
 
-template <typename E, typename Td, int NS>
+template <typename E, typename Td, int NS, int S>
 struct WideMem {
-    alignas(16) E u[2][kWideTok][32];
-    alignas(16) E z[2][kWideTok][32];
-    alignas(16) Td dt[2][kWideTok][32];
+    static constexpr int CH = 32 / S;
+    alignas(16) E u[2][kWideTok][CH];
+    alignas(16) E z[2][kWideTok][CH];
+    alignas(16) Td dt[2][kWideTok][CH];
     alignas(16) E B[2][kWideTok][NS];
     alignas(16) E C[2][kWideTok][NS];
     alignas(16) float Bf[sizeof(E) == 2 ? kWideTok : 1][NS];
@@ -164,37 +167,39 @@ __device__ __forceinline__ void widen(float (*dst)[NS], const __nv_bfloat16 (*sr
         }
     }
 }
-template <typename E>
-__device__ __forceinline__ float2 tokens_of(const E (*rows)[32], int k, int lane) {    // of tokens k and k + 1
-    return make_float2(to_float(rows[k][lane]), to_float(rows[k + 1][lane]));
+template <typename E, int CH>
+__device__ __forceinline__ float2 tokens_of(const E (*rows)[CH], int k, int ch) {      // of tokens k and k + 1
+    return make_float2(to_float(rows[k][ch]), to_float(rows[k + 1][ch]));
 }
 
-// kBlocks: more states than NS, which the inner loops then take a block at a time
-template <typename E, typename Td, int NS, bool kBlocks>
-__global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __grid_constant__ ScanParams p) {
-    constexpr int K = kWideTok, P = NS / 2, W = kWideWarps;
-    using Mem = WideMem<E, Td, NS>;
+// S: lanes of a channel, each with NS / S of the states and every S-th pair of tokens to prepare and
+// finish. kBlocks: more states than NS, which the inner loops then take a block at a time.
+template <typename E, typename Td, int NS, int S, bool kBlocks>
+__global__ void __launch_bounds__(kWideWarps * 32, kBlocks ? 9 : 6) wide_scan_kernel(const __grid_constant__ ScanParams p) {
+    constexpr int K = kWideTok, P = NS / S / 2, W = kWideWarps, CH = 32 / S, Q = K / 2 / S;
+    using Mem = WideMem<E, Td, NS, S>;
     extern __shared__ __align__(16) unsigned char smem[];
     const SelectiveArgs& a = p.a;
     const int lane = threadIdx.x & 31, warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int ch = lane % CH, j = lane / CH;             // channel, states j NS / S ..
     const int NB = kBlocks ? p.nblocks : 1;
     Mem& m = reinterpret_cast<Mem*>(smem)[warp];
     // by state block: the states entering the next tile, and (with several blocks) the rates
     float2* const carry = reinterpret_cast<float2*>(smem + W * sizeof(Mem)) + lane;     // [NB][P][32]
     float2* const rates = carry + NB * P * 32;
     const int64_t unit = blockIdx.x, per_seq = p.cblocks * a.G;
-    const int64_t seq = unit / per_seq, g = unit % per_seq / p.cblocks, c0 = unit % p.cblocks * 32;
+    const int64_t seq = unit / per_seq, g = unit % per_seq / p.cblocks, c0 = unit % p.cblocks * CH;
     const int64_t b = a.cu ? 0 : seq;
     int t0 = 0, t1 = (int)a.T;
     if (a.cu) {
         t0 = min(max(a.cu[seq], 0), t1);
         t1 = min(max(a.cu[seq + 1], 0), t1);
     }
-    const int cols = (int)min(p.per - c0, (int64_t)32);
+    const int cols = (int)min(p.per - c0, (int64_t)CH);
     const int64_t d0 = g * p.per + c0;
     const int N = (int)a.N;
-    const bool in = lane < cols;
-    const int64_t d = d0 + (in ? lane : 0);
+    const bool in = ch < cols;
+    const int64_t d = d0 + (in ? ch : 0);
     const float2 skip = both(a.Dskip ? a.Dskip[d] : 0.f), bias = both(a.dt_bias ? a.dt_bias[d] : 0.f);
     float2 A[P];
     for (int nb = 0; nb < NB; ++nb) {
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
             float v[2], r[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int n = nb * NS + 2 * i + x;
+                const int n = nb * NS + j * (2 * P) + 2 * i + x;
                 v[x] = a.init && n < N ? a.init[(seq * a.D + d) * N + n] : 0.f;
                 r[x] = n < N ? a.A[d * N + n] * kLog2e : 0.f;
             }
@@ -226,9 +231,9 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
         const int n = min(t1 - t, K);
         if (n > 0) {
             if (nb == 0) {
-                stage<K, 32>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
-                stage<K, 32>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
-                if (zb) stage<K, 32>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
+                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
             }
             stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc16);
             stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc16);
@@ -236,12 +241,12 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
         copy_commit();
     };
     const int tiles = t1 > t0 ? (t1 - t0 + K - 1) / K : 0;
-    E* const yb = static_cast<E*>(a.y) + b * a.T * a.D + d0 + lane;
+    E* const yb = static_cast<E*>(a.y) + b * a.T * a.D + d0 + ch;
     int t = t0 + warp * K, sr = 0, sb = 0;
     issue(t, 0, 0, 0);
     for (int it = warp; it < tiles; it += W, t += W * K, sr ^= 1) {
         const int n = min(t1 - t, K);
-        float2 dt[K / 2], du[K / 2], yv[K / 2];              // of two tokens each
+        float2 dt[Q], du[Q], yv[Q];                          // pair q S + j of the tile's tokens
         for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
             __syncwarp();                                    // the stage that is filled next has been read
             if (nb + 1 < NB) issue(t, nb + 1, sr ^ 1, sb ^ 1);
@@ -251,20 +256,22 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
             if (nb == 0) {
                 // past the end the step and dt u are 0, which leaves the state as it is
 #pragma unroll
-                for (int q = 0; q < K / 2; ++q) dt[q] = add_(tokens_of(m.dt[sr], 2 * q, lane), bias);
+                for (int q = 0; q < Q; ++q) dt[q] = add_(tokens_of(m.dt[sr], 2 * (q * S + j), ch), bias);
                 if (a.softplus) {
 #pragma unroll
-                    for (int q = 0; q < K / 2; ++q) dt[q] = softplus(dt[q]);
+                    for (int q = 0; q < Q; ++q) dt[q] = softplus(dt[q]);
                 }
                 if (n < K) {
 #pragma unroll
-                    for (int q = 0; q < K / 2; ++q)
-                        dt[q] = make_float2(2 * q < n ? dt[q].x : 0.f, 2 * q + 1 < n ? dt[q].y : 0.f);
+                    for (int q = 0; q < Q; ++q) {
+                        const int k = 2 * (q * S + j);
+                        dt[q] = make_float2(k < n ? dt[q].x : 0.f, k + 1 < n ? dt[q].y : 0.f);
+                    }
                 }
 #pragma unroll
-                for (int q = 0; q < K / 2; ++q) {
-                    du[q] = mul_(dt[q], tokens_of(m.u[sr], 2 * q, lane));
-                    if (kBlocks) yv[q] = both(0.f);
+                for (int q = 0; q < Q; ++q) {
+                    du[q] = mul_(dt[q], tokens_of(m.u[sr], 2 * (q * S + j), ch));
+                    yv[q] = both(0.f);
                 }
             }
             const float* Bt;
@@ -273,11 +280,11 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
                 widen<K, NS>(m.Bf, m.B[sb], lane);
                 widen<K, NS>(m.Cf, m.C[sb], lane);
                 __syncwarp();
-                Bt = &m.Bf[0][0];
-                Ct = &m.Cf[0][0];
+                Bt = &m.Bf[0][0] + j * (2 * P);
+                Ct = &m.Cf[0][0] + j * (2 * P);
             } else {
-                Bt = &m.B[sb][0][0];
-                Ct = &m.C[sb][0][0];
+                Bt = &m.B[sb][0][0] + j * (2 * P);
+                Ct = &m.C[sb][0][0] + j * (2 * P);
             }
             // barrier w: the other warp has run its tile, whose states are in carry
             if (nb == 0 && it > 0) pair_wait<W>(warp);
@@ -289,8 +296,13 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
             }
             // a token's decays, B and C while the states of the one before are computed
             float2 e[2][P], Bv[2][P], Cv[2][P];
+            // a value of token k out of the pairs, from the lane that has it
+            auto of = [&](const float2 (&v)[Q], int k) {
+                const float x = k % 2 ? v[k / 2 / S].y : v[k / 2 / S].x;
+                return S == 1 ? x : __shfl_sync(0xffffffffu, x, k / 2 % S * CH + ch);
+            };
             auto prepare = [&](int k) {
-                const float st = k % 2 ? dt[k / 2].y : dt[k / 2].x;
+                const float st = of(dt, k);
 #pragma unroll
                 for (int i = 0; i < P; i += 2) {
                     quad_of(Bt + k * NS + 2 * i, Bv[k & 1] + i);
@@ -299,10 +311,11 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < P; ++i) e[k & 1][i] = ex2(mul_(both(st), A[i]));
             };
+            float part[2 * S];                               // of y, for S pairs of tokens
             prepare(0);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                const float su = k % 2 ? du[k / 2].y : du[k / 2].x;
+                const float su = of(du, k);
                 if (k + 1 < K) prepare(k + 1);
                 float2 r[2] = {both(0.f), both(0.f)};
 #pragma unroll
@@ -311,52 +324,68 @@ __global__ void __launch_bounds__(kWideWarps * 32, 6) wide_scan_kernel(const __g
                     r[i & 1] = fma_(Cv[k & 1][i], h[i], r[i & 1]);
                 }
                 r[0] = add_(r[0], r[1]);
-                float& y = k % 2 ? yv[k / 2].y : yv[k / 2].x;
-                y = kBlocks ? y + (r[0].x + r[0].y) : r[0].x + r[0].y;
+                part[k % (2 * S)] = r[0].x + r[0].y;
+                if (k % (2 * S) == 2 * S - 1) {              // each lane keeps its pair's sum
+                    float2 v = make_float2(part[0], part[1]);
+                    if constexpr (S == 2) {
+                        const float2 o = make_float2(part[2], part[3]);
+                        const float2 send = j ? v : o;
+                        v = add_(j ? o : v, make_float2(__shfl_xor_sync(0xffffffffu, send.x, CH),
+                                                        __shfl_xor_sync(0xffffffffu, send.y, CH)));
+                    }
+                    yv[k / (2 * S)] = kBlocks ? add_(yv[k / (2 * S)], v) : v;
+                }
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) carry[(nb * P + i) * 32] = h[i];
         }
         if (it + 1 < tiles) pair_arrive<W>(warp ^ 1);
 #pragma unroll
-        for (int q = 0; q < K / 2; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * q, lane), yv[q]);
+        for (int q = 0; q < Q; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
         if (zb) {
 #pragma unroll
-            for (int q = 0; q < K / 2; ++q) yv[q] = mul_(yv[q], silu(tokens_of(m.z[sr], 2 * q, lane)));
+            for (int q = 0; q < Q; ++q) yv[q] = mul_(yv[q], silu(tokens_of(m.z[sr], 2 * (q * S + j), ch)));
         }
-        E* to = yb + (int64_t)t * (int)a.D;
-        if (n == K && cols == 32) {
+        E* to = yb + (int64_t)(t + 2 * j) * (int)a.D;
+        if (n == K && cols == CH) {
 #pragma unroll
-            for (int q = 0; q < K / 2; ++q, to += 2 * a.D) {
+            for (int q = 0; q < Q; ++q, to += 2 * S * a.D) {
                 store_elem(to, yv[q].x);
                 store_elem(to + a.D, yv[q].y);
             }
         } else if (in) {
 #pragma unroll
-            for (int q = 0; q < K / 2; ++q, to += 2 * a.D) {
-                if (2 * q < n) store_elem(to, yv[q].x);
-                if (2 * q + 1 < n) store_elem(to + a.D, yv[q].y);
+            for (int q = 0; q < Q; ++q, to += 2 * S * a.D) {
+                const int k = 2 * (q * S + j);
+                if (k < n) store_elem(to, yv[q].x);
+                if (k + 1 < n) store_elem(to + a.D, yv[q].y);
             }
         }
     }
     copy_wait<0>();
     // the warp that wrote the carried states last
     if (!a.fin || !in || warp != (tiles == 0 ? 0 : (tiles - 1) % W)) return;
-    for (int n = 0; n < N; ++n) {
-        const float2 h = carry[n / 2 * 32];
-        a.fin[(seq * a.D + d) * N + n] = n % 2 ? h.y : h.x;
+    for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const float2 h = carry[(nb * P + i) * 32];
+            const int n = nb * NS + j * (2 * P) + 2 * i;
+            if (n < N) a.fin[(seq * a.D + d) * N + n] = h.x;
+            if (n + 1 < N) a.fin[(seq * a.D + d) * N + n + 1] = h.y;
+        }
     }
 }
 
-template <typename E, typename Td, int NS, bool kBlocks>
+template <typename E, typename Td, int NS, int S, bool kBlocks>
 cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     const SelectiveArgs& a = p.a;
-    p.cblocks = (p.per + 31) / 32;
+    p.cblocks = (p.per + 32 / S - 1) / (32 / S);
     p.nblocks = (int)((a.N + NS - 1) / NS);
     const int64_t units = a.nseq * a.G * p.cblocks;
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t shared = kWideWarps * sizeof(WideMem<E, Td, NS>) + (size_t)p.nblocks * NS * 32 * 4 * (p.nblocks > 1 ? 2 : 1);
-    auto kernel = wide_scan_kernel<E, Td, NS, kBlocks>;
+    const size_t shared = kWideWarps * sizeof(WideMem<E, Td, NS, S>) +
+                          (size_t)p.nblocks * (NS / S) * 32 * 4 * (p.nblocks > 1 ? 2 : 1);
+    auto kernel = wide_scan_kernel<E, Td, NS, S, kBlocks>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
@@ -699,13 +728,16 @@ cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
     const SelectiveArgs& a = p.a;
     const int64_t cblocks = (p.per + CH - 1) / CH, units = a.nseq * a.G * cblocks;
     const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
-    // One wave of CTAs is the cut form's (one of 16 warps or two of 8 on each SM): beyond it, and for
-    // short sequences, the uncut form (2048 tokens, 16 states, bf16: 4096 channels 106 us cut, 171
-    // uncut; 8192 channels 207 cut, 175 uncut).
-    if (units > 2 * 148 || len <= 8 * kCutTok) {
-        if constexpr (SL == 4)
-            if (a.N > NS) return launch_wide<E, Td, NS, true>(p, st);
-        return launch_wide<E, Td, NS, false>(p, st);
+    // The cut form's 16 warps fill an SM, so it is for units that one wave takes (2048 tokens, 16 states,
+    // bf16: 2048 channels 58 us cut, 100 uncut; 3200 channels 107 cut, 102 uncut), and for sequences of
+    // a round or more. More states than a lane holds make up for few channels, and the uncut form reads
+    // their B and C a block at a time (64 states: 1024 tokens of 10240 channels 458 us cut, 516 uncut;
+    // 512 tokens of 81920 channels 1537 cut, 1215 uncut).
+    constexpr int S = NS >= 8 ? 2 : 1;
+    if (a.N <= NS) {
+        if (units > 148 || len <= 8 * kCutTok) return launch_wide<E, Td, NS, S, false>(p, st);
+    } else if constexpr (SL == 4) {
+        if (units > 6 * 148) return launch_wide<E, Td, NS, S, true>(p, st);
     }
     p.cblocks = cblocks;
     p.nblocks = (int)((a.N + NS - 1) / NS);
