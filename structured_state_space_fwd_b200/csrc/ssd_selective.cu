@@ -16,8 +16,9 @@
 // Two forms, both with their inputs copied asynchronously a tile ahead:
 //   many channels (wide_scan_kernel): a lane holds the states of a channel, nothing is exchanged
 //     between lanes, and two warps take the tiles of a block of channels in turn;
-//   few channels (cut_scan_kernel): four lanes share a pair of channels, and the warps of a CTA take
-//     consecutive runs of tokens of the same channels.
+//   few channels (cut_scan_kernel): lanes share pairs of channels, and the warps of a CTA take
+//     consecutive runs of tokens of the same channels; for very few, the CTAs of a cluster take
+//     consecutive segments.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -36,7 +37,7 @@ struct ScanParams {
     int64_t per;                 // channels of a group
     int64_t cblocks;             // channel blocks of a group
     int nblocks;                 // state blocks
-    bool rows16, bc16;           // u, dt, z (B, C) take 16-byte copies
+    int row_bytes, bc_bytes;     // pieces in which u, dt, z (B, C) are copied: 16, 4 or one element
     bool y_pairs;                // y takes stores of two channels
 };
 
@@ -75,38 +76,80 @@ __device__ __forceinline__ void pair_wait(int id) {
 #undef SSD_WAIT
 }
 
+// The CTAs of a cluster: rank, a barrier in two halves, and loads from another CTA's shared memory.
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ int cluster_size() {
+    int r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t in_cta(const void* own, int rank) {     // the same place in CTA `rank`
+    uint32_t at;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(own)), "r"(rank));
+    return at;
+}
+__device__ __forceinline__ float4 remote4(uint32_t at) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 remote2(uint32_t at) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
 // Copies K rows of W elements, row stride `row`, to shared memory [K][W], zeros where the row is not
-// below `rows` or the column not below `cols`. wide: in 16-byte pieces (a piece is then inside or
-// outside as a whole).
+// below `rows` or the column not below `cols`, in pieces of `bytes`: 16 or 4 asynchronously (a piece is
+// then inside or outside as a whole), else element by element.
 template <int K, int W, typename E>
-__device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, int cols, int lane, bool wide) {
+__device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, int cols, int lane, int bytes) {
     constexpr int V = 16 / sizeof(E), P = W >= V ? W / V : 1, kPieces = (K * P + 31) / 32;
-    if (W >= V && wide) {
+    if (W >= V && bytes == 16) {
         const int k0 = lane / P, c = (lane % P) * V;
         const E* from = src + ((int64_t)k0 * row + c);
         if (rows == K && cols >= W) {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i)
-                if (K * P % 32 == 0 || k0 < K) copy16(dst + (k0 + i * (32 / P)) * W + c, from + (int64_t)(i * (32 / P)) * row, true);
+                if (K * P % 32 == 0 || k0 < K)
+                    copy16(dst + (k0 + i * (32 / P)) * W + c, from + (int64_t)(i * (32 / P)) * row, true);
         } else {
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int k = k0 + i * (32 / P);
                 const bool ok = k < rows && c < cols;
-                if (K * P % 32 == 0 || k < K) copy16(dst + k * W + c, ok ? from + (int64_t)(i * (32 / P)) * row : src, ok);
+                if (K * P % 32 == 0 || k < K)
+                    copy16(dst + k * W + c, ok ? from + (int64_t)(i * (32 / P)) * row : src, ok);
             }
+        }
+    } else if (bytes >= 4) {
+        constexpr int V4 = 4 / sizeof(E), P4 = W / V4;
+#pragma unroll
+        for (int i = 0; i < (K * P4 + 31) / 32; ++i) {
+            const int k = (lane + 32 * i) / P4, c = (lane + 32 * i) % P4 * V4;
+            const bool ok = k < rows && c < cols;
+            if (K * P4 % 32 == 0 || k < K) copy4(dst + k * W + c, ok ? src + ((int64_t)k * row + c) : src, ok);
         }
     } else {
-#pragma unroll 2
-        for (int idx = lane; idx < K * W; idx += 32) {
-            const int k = idx / W, c = idx % W;
-            const bool ok = k < rows && c < cols;
-            if constexpr (sizeof(E) == 4) {
-                copy4(dst + idx, ok ? src + ((int64_t)k * row + c) : src, ok);
-            } else {
-                dst[idx] = ok ? src[(int64_t)k * row + c] : E(0.f);
-            }
+        constexpr int kN = (K * W + 31) / 32;
+        E v[kN];                                          // all loads before the first store
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int k = (lane + 32 * i) / W, c = (lane + 32 * i) % W;
+            v[i] = k < rows && c < cols ? src[(int64_t)k * row + c] : E(0.f);
         }
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            if (K * W % 32 == 0 || lane + 32 * i < K * W) dst[lane + 32 * i] = v[i];
     }
 }
 
@@ -231,12 +274,12 @@ __global__ void __launch_bounds__(kWideWarps * 32, kBlocks ? 9 : 6) wide_scan_ke
         const int n = min(t1 - t, K);
         if (n > 0) {
             if (nb == 0) {
-                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
-                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
-                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.row_bytes);
+                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.row_bytes);
+                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.row_bytes);
             }
-            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc16);
-            stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc_bytes);
+            stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc_bytes);
         }
         copy_commit();
     };
@@ -409,6 +452,13 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
 // state a warp adds sum_n (C_t prod a)[n] h[n] to each y_t, at two packed operations per pair of
 // states and no second exponential. 16384 tokens of 2048 channels, 16 states, fp32: 8 warps 526 us,
 // 16 warps 379 (no cut: 1308).
+//
+// kSegments: with so few channels that most SMs would stay empty, a cluster of CTAs shares a unit's
+// tokens, a segment each. Every CTA first runs its segment from a state of zero, without outputs, to
+// what it leaves and the sum of its steps, whose exponential with A is its decay; after one barrier of
+// the cluster each folds the segments before its own, over distributed shared memory, into its
+// entering states, and runs its segment again with outputs. The exponentials are computed twice, on
+// SMs that had none.
 constexpr int kCutTok = 8;       // 8 floats a token and lane are kept
 
 template <typename E, typename Td, int SL>
@@ -439,7 +489,7 @@ struct States {
     }
 };
 
-template <typename E, typename Td, int SL, int W>
+template <typename E, typename Td, int SL, int W, bool kSegments>
 __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kCutTok;
     constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
@@ -450,18 +500,31 @@ __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_c
     const int cp = lane % CL, j = lane / CL;             // pair of channels, states 4 j ..
     const int NB = p.nblocks;
     Mem& m = reinterpret_cast<Mem*>(smem)[warp];
-    // the states entering the next round of W tiles, by state block; two slots a warp for what its
-    // predecessor hands over
+    // by state block: the states entering the next round of W tiles; two slots a warp for what its
+    // predecessor hands over. Segments: also what the segment leaves from a state of zero, and the sums
+    // of its steps on their way from warp to warp.
     float4* const carry = reinterpret_cast<float4*>(smem + W * sizeof(Mem));
     float4* const slots = carry + NB * 64;
+    float4* const leaves = slots + 2 * W * 64;
+    float2* const sums = reinterpret_cast<float2*>(leaves + NB * 64);                   // [2 W + 1][32]
 
-    const int64_t unit = blockIdx.x, per_seq = p.cblocks * a.G;
+    const int rank = kSegments ? cluster_rank() : 0, ranks = kSegments ? cluster_size() : 1;
+    const int64_t unit = blockIdx.x / ranks, per_seq = p.cblocks * a.G;
     const int64_t seq = unit / per_seq, g = unit % per_seq / p.cblocks, c0 = unit % p.cblocks * CH;
     const int64_t b = a.cu ? 0 : seq;
     int t0 = 0, t1 = (int)a.T;
     if (a.cu) {
         t0 = min(max(a.cu[seq], 0), t1);
         t1 = min(max(a.cu[seq + 1], 0), t1);
+    }
+    // the CTA's segment: whole rounds, as many for each rank but the last ones
+    bool last = true;                                    // whether the sequence ends here
+    if constexpr (kSegments) {
+        const int end = t1, part = (max(t1 - t0, 0) + ranks * W * K - 1) / (ranks * W * K) * (W * K);
+        const int64_t from = t0 + (int64_t)rank * part;
+        last = end > t0 ? from < end && from + part >= end : rank == 0;
+        t1 = (int)min((int64_t)end, from + part);
+        t0 = (int)min((int64_t)max(end, t0), from);
     }
     const int cols = (int)min(p.per - c0, (int64_t)CH);
     const int64_t d0 = g * p.per + c0;
@@ -481,14 +544,19 @@ __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_c
         lo = make_float2(v[0], v[1]);
         hi = make_float2(v[2], v[3]);
     };
+    const float* const init = a.init ? a.init + seq * a.D * N : nullptr;
     if (warp == 0) {
-        const float* const init = a.init ? a.init + seq * a.D * N : nullptr;
         for (int nb = 0; nb < NB; ++nb) {
             States h;
             row_of(init, da, nb, 1.f, h.v[0][0], h.v[0][1]);
             row_of(init, db, nb, 1.f, h.v[1][0], h.v[1][1]);
             h.store(carry + nb * 64 + lane);
+            if (kSegments) {
+                h.fill(0.f);
+                h.store(leaves + nb * 64 + lane);
+            }
         }
+        if (kSegments) sums[2 * W * 32 + lane] = both(0.f);
     }
 
     const E* const ub = static_cast<const E*>(a.u) + b * a.us.batch + d0;
@@ -498,16 +566,16 @@ __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_c
     const E* const Cb = static_cast<const E*>(a.C) + b * a.Cs.batch + g * N;
     const int ur = (int)a.us.row, dtr = (int)a.dts.row, zr = (int)a.zs.row, Br = (int)a.Bs.row, Cr = (int)a.Cs.row;
     // the copies of the tile at token t, state block nb; u, dt, z (stage sr) with the first block
-    auto issue = [&](int t, int nb, int sr, int sb) {
+    auto issue = [&](int t, int nb, int sr, int sb, bool out) {
         const int n = min(t1 - t, K);
         if (n > 0) {
             if (nb == 0) {
-                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.rows16);
-                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.rows16);
-                if (zb) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.rows16);
+                stage<K, CH>(&m.u[sr][0][0], ub + (int64_t)t * ur, ur, n, cols, lane, p.row_bytes);
+                stage<K, CH>(&m.dt[sr][0][0], dtb + (int64_t)t * dtr, dtr, n, cols, lane, p.row_bytes);
+                if (zb && out) stage<K, CH>(&m.z[sr][0][0], zb + (int64_t)t * zr, zr, n, cols, lane, p.row_bytes);
             }
-            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc16);
-            stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc16);
+            stage<K, NS>(&m.B[sb][0][0], Bb + (int64_t)t * Br + nb * NS, Br, n, N - nb * NS, lane, p.bc_bytes);
+            if (out) stage<K, NS>(&m.C[sb][0][0], Cb + (int64_t)t * Cr + nb * NS, Cr, n, N - nb * NS, lane, p.bc_bytes);
         }
         copy_commit();
     };
@@ -544,187 +612,245 @@ __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_c
         row_of(a.A, db, nb, kLog2e, A.v[1][0], A.v[1][1]);
     };
     if (NB == 1) rates(0);
-    int t = t0 + warp * K, sr = 0, sb = 0;
-    if (rounds > 0) issue(t, 0, 0, 0);
-    for (int it = 0; it < rounds; ++it, t += W * K, sr ^= 1) {
-        const int n = min(t1 - t, K);
-        for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
-            __syncwarp();                                // the stage that is filled next has been read
-            if (nb + 1 < NB)
-                issue(t, nb + 1, sr ^ 1, sb ^ 1);
-            else if (it + 1 < rounds)
-                issue(t + W * K, 0, sr ^ 1, sb ^ 1);
-            else
-                copy_commit();
-            copy_wait<1>();
-            __syncwarp();
-            if (NB > 1) rates(nb);
-            if (n > 0) {
+    // The segment's rounds; kOut: with outputs, from the states in `carry`, else only what it leaves
+    // from zero, in `leaves`, and the sum of its steps.
+    auto run = [&](auto out, float4* const carry) {
+        constexpr bool kOut = decltype(out)::value;
+        int t = t0 + warp * K, sr = 0, sb = 0;
+        if (rounds > 0) issue(t, 0, 0, 0, kOut);
+        for (int it = 0; it < rounds; ++it, t += W * K, sr ^= 1) {
+            const int n = min(t1 - t, K);
+            for (int nb = 0; nb < NB; ++nb, sb ^= 1) {
+                __syncwarp();                                // the stage that is filled next has been read
+                if (nb + 1 < NB)
+                    issue(t, nb + 1, sr ^ 1, sb ^ 1, kOut);
+                else if (it + 1 < rounds)
+                    issue(t + W * K, 0, sr ^ 1, sb ^ 1, kOut);
+                else
+                    copy_commit();
+                copy_wait<1>();
+                __syncwarp();
+                if (NB > 1) rates(nb);
+                if (n > 0) {
+                    if (nb == 0) {
+                        // once per (token, channel): the step and dt u; past the end both are 0, which
+                        // leaves the state as it is
+                        float2 v[K / SL];
+#pragma unroll
+                        for (int q = 0; q < K / SL; ++q) v[q] = add_(pair_of(&m.dt[sr][q * SL + j][2 * cp]), bias);
+                        if (a.softplus) {
+#pragma unroll
+                            for (int q = 0; q < K / SL; ++q) v[q] = softplus(v[q]);
+                        }
+                        if (n < K) {
+#pragma unroll
+                            for (int q = 0; q < K / SL; ++q) v[q] = q * SL + j < n ? v[q] : both(0.f);
+                        }
+#pragma unroll
+                        for (int q = 0; q < K / SL; ++q) {
+                            const float2 du = mul_(v[q], pair_of(&m.u[sr][q * SL + j][2 * cp]));
+                            m.s[q * SL + j][cp] = make_float4(v[q].x, du.x, v[q].y, du.y);
+                        }
+                    }
+                    __syncwarp();
+                }
                 if (nb == 0) {
-                    // once per (token, channel): the step and dt u; past the end both are 0, which
-                    // leaves the state as it is
-                    float2 v[K / SL];
 #pragma unroll
-                    for (int q = 0; q < K / SL; ++q) v[q] = add_(pair_of(&m.dt[sr][q * SL + j][2 * cp]), bias);
-                    if (a.softplus) {
+                    for (int q = 0; q < K / SL; ++q) ysum[q] = both(0.f);
+                }
+                States h, decay;
+                float2 steps = both(0.f);                    // sum of the tile's
+                float2 gc[K][2][2];               // C_t times the decays up to t
+                decay.fill(1.f);
+                h.fill(0.f);
+                if (n > 0) {
+                    const E* const Bt = &m.B[sb][0][0] + j * 4;
+                    const E* const Ct = &m.C[sb][0][0] + j * 4;
+                    // exps of the next token ahead of the states of this one
+                    float2 e[2][2][2];
+                    float4 sk = m.s[0][cp];
+                    auto exps = [&](float2 (&to)[2][2], const float4& s) {
 #pragma unroll
-                        for (int q = 0; q < K / SL; ++q) v[q] = softplus(v[q]);
-                    }
-                    if (n < K) {
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int q = 0; q < K / SL; ++q) v[q] = q * SL + j < n ? v[q] : both(0.f);
-                    }
+                            for (int i = 0; i < 2; ++i) to[c][i] = ex2(mul_(both(c ? s.z : s.x), A.v[c][i]));
+                    };
+                    exps(e[0], sk);
 #pragma unroll
-                    for (int q = 0; q < K / SL; ++q) {
-                        const float2 du = mul_(v[q], pair_of(&m.u[sr][q * SL + j][2 * cp]));
-                        m.s[q * SL + j][cp] = make_float4(v[q].x, du.x, v[q].y, du.y);
+                    for (int k = 0; k < K; ++k) {
+                        const float4 s = sk;
+                        float2 Bv[2], Cv[2];
+                        quad_of(Bt + k * NS, Bv);
+                        if (kOut) quad_of(Ct + k * NS, Cv);
+                        if (k + 1 < K) {
+                            sk = m.s[k + 1][cp];
+                            exps(e[(k + 1) & 1], sk);
+                        }
+                        float part[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float2 du = both(c ? s.w : s.y);
+                            float2 r = both(0.f);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const float2 ek = e[k & 1][c][i];
+                                h.v[c][i] = fma_(ek, h.v[c][i], mul_(du, Bv[i]));
+                                decay.v[c][i] = k ? mul_(decay.v[c][i], ek) : ek;
+                                if constexpr (kOut) {
+                                    r = i ? fma_(Cv[i], h.v[c][i], r) : mul_(Cv[i], h.v[c][i]);
+                                    gc[k][c][i] = mul_(Cv[i], decay.v[c][i]);
+                                }
+                            }
+                            part[c] = r.x + r.y;
+                        }
+                        if constexpr (kOut) yv[k] = make_float2(part[0], part[1]);
+                        else steps = add_(steps, make_float2(s.x, s.z));
                     }
                 }
-                __syncwarp();
-            }
-            if (nb == 0) {
+                // The entering state: the first warp's is what the last one left of the round before,
+                // any other's comes from its predecessor (barrier w, and slot w by parity). The first
+                // warp is told once a round. With one state block a predecessor cannot come to its
+                // next hand-over before this one has gone round the chain, and need not wait; with
+                // several, both wait, and the second slot keeps the next hand-over off this one.
+                float4* const slot = slots + (((it * NB + nb) & 1) * W + warp) * 64 + lane;
+                if (warp == 0) {
+                    if (it > 0 && nb == 0) pair_wait<W>(0);
+                } else {
+                    pair_wait<W>(warp);
+                }
+                States in;
+                in.load(warp == 0 ? carry + nb * 64 + lane : slot);
 #pragma unroll
-                for (int q = 0; q < K / SL; ++q) ysum[q] = both(0.f);
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) h.v[c][i] = fma_(decay.v[c][i], in.v[c][i], h.v[c][i]);
+                if constexpr (!kOut) {
+                    if (nb == 0) {
+                        float2* const sum = sums + (it & 1) * W * 32 + lane;
+                        steps = add_(steps, warp == 0 ? sums[2 * W * 32 + lane] : sum[warp * 32]);
+                        (warp + 1 < W ? sum[(warp + 1) * 32] : sums[2 * W * 32 + lane]) = steps;
+                    }
+                }
+                if (warp + 1 < W) {
+                    h.store(slot + 64);
+                    if (NB == 1) pair_arrive<W>(warp + 1);
+                    else pair_wait<W>(warp + 1);
+                } else {
+                    h.store(carry + nb * 64 + lane);
+                    if (nb == NB - 1 && it + 1 < rounds) pair_arrive<W>(0);
+                }
+                if (kOut && n > 0) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        float part[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float2 r =
+                                fma_(gc[k][c][1], in.v[c][1], mul_(gc[k][c][0], in.v[c][0]));
+                            part[c] = r.x + r.y;
+                        }
+                        yv[k] = add_(yv[k], make_float2(part[0], part[1]));
+                        if (k % SL == SL - 1) gather(k / SL);
+                    }
+                }
             }
-            States h, decay;
-            float2 gc[K][2][2];               // C_t times the decays up to t
-            decay.fill(1.f);
-            h.fill(0.f);
-            if (n > 0) {
-                const E* const Bt = &m.B[sb][0][0] + j * 4;
-                const E* const Ct = &m.C[sb][0][0] + j * 4;
-                // exps of the next token ahead of the states of this one
-                float2 e[2][2][2];
-                float4 sk = m.s[0][cp];
-                auto exps = [&](float2 (&to)[2][2], const float4& s) {
+            if (!kOut || n <= 0) continue;
+            E* to = yb + (int64_t)(t + j) * (int)Dr;
+            const int64_t step = SL * Dr;
+#pragma unroll
+            for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+            if (zb) {
+#pragma unroll
+                for (int q = 0; q < K / SL; ++q) ysum[q] = mul_(ysum[q], silu(pair_of(&m.z[sr][q * SL + j][2 * cp])));
+            }
+            if (n == K && cols == CH && p.y_pairs) {
+#pragma unroll
+                for (int q = 0; q < K / SL; ++q, to += step) store_pair(to, ysum[q]);
+            } else {
+#pragma unroll
+                for (int q = 0; q < K / SL; ++q, to += step)
+                    if (q * SL + j < n) {
+                        if (in0) store_elem(to, ysum[q].x);
+                        if (in1) store_elem(to + 1, ysum[q].y);
+                    }
+            }
+        }
+        copy_wait<0>();
+    };
+    if constexpr (kSegments) {
+        // What each segment leaves, then the fold of those before this one: the entering state
+        run(std::false_type{}, leaves);
+        cluster_arrive();
+        cluster_wait();
+        if (warp == 0) {
+            for (int nb = 0; nb < NB; ++nb) {
+                States h;
+                h.load(carry + nb * 64 + lane);
+                rates(nb);
+                for (int q = 0; q < rank; ++q) {
+                    const float2 sum = remote2(in_cta(sums + 2 * W * 32 + lane, q));
+                    const uint32_t at = in_cta(leaves + nb * 64 + lane, q);
+                    const float4 l0 = remote4(at), l1 = remote4(at + 32 * 16);
+                    const float2 l[2][2] = {{make_float2(l0.x, l0.y), make_float2(l0.z, l0.w)},
+                                            {make_float2(l1.x, l1.y), make_float2(l1.z, l1.w)}};
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) to[c][i] = ex2(mul_(both(c ? s.z : s.x), A.v[c][i]));
-                };
-                exps(e[0], sk);
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    const float4 s = sk;
-                    float2 Bv[2], Cv[2];
-                    quad_of(Bt + k * NS, Bv);
-                    quad_of(Ct + k * NS, Cv);
-                    if (k + 1 < K) {
-                        sk = m.s[k + 1][cp];
-                        exps(e[(k + 1) & 1], sk);
-                    }
-                    float part[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float2 du = both(c ? s.w : s.y);
-                        float2 r = both(0.f);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float2 ek = e[k & 1][c][i];
-                            h.v[c][i] = fma_(ek, h.v[c][i], mul_(du, Bv[i]));
-                            r = i ? fma_(Cv[i], h.v[c][i], r) : mul_(Cv[i], h.v[c][i]);
-                            decay.v[c][i] = k ? mul_(decay.v[c][i], ek) : ek;
-                            gc[k][c][i] = mul_(Cv[i], decay.v[c][i]);
-                        }
-                        part[c] = r.x + r.y;
-                    }
-                    yv[k] = make_float2(part[0], part[1]);
+                        for (int i = 0; i < 2; ++i)
+                            h.v[c][i] = fma_(ex2(mul_(both(c ? sum.y : sum.x), A.v[c][i])), h.v[c][i], l[c][i]);
                 }
-            }
-            // The entering state: the first warp's is what the last one left of the round before,
-            // any other's comes from its predecessor (barrier w, and slot w by parity). The first
-            // warp is told once a round. With one state block a predecessor cannot come to its
-            // next hand-over before this one has gone round the chain, and need not wait; with
-            // several, both wait, and the second slot keeps the next hand-over off this one.
-            float4* const slot = slots + (((it * NB + nb) & 1) * W + warp) * 64 + lane;
-            if (warp == 0) {
-                if (it > 0 && nb == 0) pair_wait<W>(0);
-            } else {
-                pair_wait<W>(warp);
-            }
-            States in;
-            in.load(warp == 0 ? carry + nb * 64 + lane : slot);
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) h.v[c][i] = fma_(decay.v[c][i], in.v[c][i], h.v[c][i]);
-            if (warp + 1 < W) {
-                h.store(slot + 64);
-                if (NB == 1) pair_arrive<W>(warp + 1);
-                else pair_wait<W>(warp + 1);
-            } else {
                 h.store(carry + nb * 64 + lane);
-                if (nb == NB - 1 && it + 1 < rounds) pair_arrive<W>(0);
-            }
-            if (n > 0) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) {
-                    float part[2];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float2 r =
-                            fma_(gc[k][c][1], in.v[c][1], mul_(gc[k][c][0], in.v[c][0]));
-                        part[c] = r.x + r.y;
-                    }
-                    yv[k] = add_(yv[k], make_float2(part[0], part[1]));
-                    if (k % SL == SL - 1) gather(k / SL);
-                }
             }
         }
-        if (n <= 0) continue;
-        E* to = yb + (int64_t)(t + j) * (int)Dr;
-        const int64_t step = SL * Dr;
-#pragma unroll
-        for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
-        if (zb) {
-#pragma unroll
-            for (int q = 0; q < K / SL; ++q) ysum[q] = mul_(ysum[q], silu(pair_of(&m.z[sr][q * SL + j][2 * cp])));
-        }
-        if (n == K && cols == CH && p.y_pairs) {
-#pragma unroll
-            for (int q = 0; q < K / SL; ++q, to += step) store_pair(to, ysum[q]);
-        } else {
-#pragma unroll
-            for (int q = 0; q < K / SL; ++q, to += step)
-                if (q * SL + j < n) {
-                    if (in0) store_elem(to, ysum[q].x);
-                    if (in1) store_elem(to + 1, ysum[q].y);
-                }
-        }
+        cluster_arrive();
     }
-    copy_wait<0>();
+    run(std::true_type{}, carry);
     // the warp that wrote the carried states last
-    if (!a.fin || warp != (rounds == 0 ? 0 : W - 1)) return;
-    for (int nb = 0; nb < NB; ++nb) {
-        States h;
-        h.load(carry + nb * 64 + lane);
+    if (a.fin && last && warp == (rounds == 0 ? 0 : W - 1)) {
+        for (int nb = 0; nb < NB; ++nb) {
+            States h;
+            h.load(carry + nb * 64 + lane);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const float v[4] = {h.v[c][0].x, h.v[c][0].y, h.v[c][1].x, h.v[c][1].y};
+            for (int c = 0; c < 2; ++c) {
+                const float v[4] = {h.v[c][0].x, h.v[c][0].y, h.v[c][1].x, h.v[c][1].y};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = nb * NS + j * 4 + i;
-                if (n < N && (c ? in1 : in0)) a.fin[(seq * a.D + (c ? db : da)) * N + n] = v[i];
+                for (int i = 0; i < 4; ++i) {
+                    const int n = nb * NS + j * 4 + i;
+                    if (n < N && (c ? in1 : in0)) a.fin[(seq * a.D + (c ? db : da)) * N + n] = v[i];
+                }
             }
         }
     }
+    if constexpr (kSegments) cluster_wait();             // others read this CTA's shared memory until here
 }
 
-template <typename E, typename Td, int SL, int W>
-cudaError_t launch_cut(const ScanParams& p, int64_t units, cudaStream_t st) {
-    const size_t shared = W * sizeof(CutMem<E, Td, SL>) + (size_t)(p.nblocks + 2 * W) * 64 * 16;
-    auto kernel = cut_scan_kernel<E, Td, SL, W>;
+template <typename E, typename Td, int SL, int W, bool kSegments>
+cudaError_t launch_cut(const ScanParams& p, int64_t units, int ranks, cudaStream_t st) {
+    const size_t shared = W * sizeof(CutMem<E, Td, SL>) + (size_t)(p.nblocks + 2 * W) * 64 * 16 +
+                          (kSegments ? (size_t)p.nblocks * 64 * 16 + (2 * W + 1) * 32 * 8 : 0);
+    auto kernel = cut_scan_kernel<E, Td, SL, W, kSegments>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<(unsigned)units, W * 32, shared, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = (unsigned)ranks;
+    cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3((unsigned)(units * ranks));
+    config.blockDim = dim3(W * 32);
+    config.dynamicSmemBytes = shared;
+    config.stream = st;
+    config.attrs = &cluster;
+    config.numAttrs = kSegments ? 1 : 0;
+    return cudaLaunchKernelEx(&config, kernel, p);
 }
 
-template <typename E, typename Td, int SL>
+// SL: lanes for a pair of channels in the cut form; NS: states of a channel's lanes in the uncut one
+template <typename E, typename Td, int SL, int NS>
 cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
-    constexpr int CH = 64 / SL, NS = 4 * SL;
+    constexpr int CH = 64 / SL;
     const SelectiveArgs& a = p.a;
     const int64_t cblocks = (p.per + CH - 1) / CH, units = a.nseq * a.G * cblocks;
     const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
@@ -740,12 +866,18 @@ cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
         if (units > 6 * 148) return launch_wide<E, Td, NS, S, true>(p, st);
     }
     p.cblocks = cblocks;
-    p.nblocks = (int)((a.N + NS - 1) / NS);
-    // 16 warps where the shared memory of one CTA has room for them
-    constexpr bool kFits = 16 * sizeof(CutMem<E, Td, SL>) <= 160 * 1024;
-    if constexpr (kFits)
-        if (units <= 148 && len > 128) return launch_cut<E, Td, SL, 16>(p, units, st);
-    return launch_cut<E, Td, SL, 8>(p, units, st);
+    p.nblocks = (int)((a.N + 4 * SL - 1) / (4 * SL));
+    if (units <= 148 && len > 128) {
+        const int64_t rounds = (len + 16 * kCutTok - 1) / (16 * kCutTok);
+        // Clusters of 8 and 4 such CTAs as long as the GPU has them at once (SMs of one cluster lie
+        // together) and the segments have a round each (15 states, bf16, 6720 tokens of 2 x 16 channels:
+        // 214 us without, 59 with 8; 16 states, 8192 tokens of 512 channels: 218 without, 118 with 4).
+        // Two segments would gain nothing, at 1.6 times the work.
+        if (units <= 12 && rounds >= 8) return launch_cut<E, Td, SL, 16, true>(p, units, 8, st);
+        if (units <= 32 && rounds >= 4) return launch_cut<E, Td, SL, 16, true>(p, units, 4, st);
+        return launch_cut<E, Td, SL, 16, false>(p, units, 1, st);
+    }
+    return launch_cut<E, Td, SL, 8, false>(p, units, 1, st);
 }
 
 template <typename E, typename Td>
@@ -754,16 +886,17 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
     ScanParams p = {};
     p.a = a;
     p.per = a.D / a.G;
-    const int64_t v = 16 / sizeof(E), vd = 16 / sizeof(Td);
-    auto ok = [](const void* q, const ssd_strides_t& s, int64_t n) {
-        return aligned(q, 16) && s.batch % n == 0 && s.row % n == 0;
+    auto pieces = [](const void* q, const ssd_strides_t& s, int64_t inner, int64_t es) {   // 16, 4 or less
+        const int64_t all = (int64_t)(uintptr_t)q | s.batch * es | s.row * es | inner * es;
+        return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : (int)es;
     };
-    p.rows16 = p.per % v == 0 && ok(a.u, a.us, v) && ok(a.dt, a.dts, vd) && (!a.z || ok(a.z, a.zs, v));
-    p.bc16 = a.N % v == 0 && ok(a.B, a.Bs, v) && ok(a.C, a.Cs, v);
+    p.row_bytes = std::min(pieces(a.u, a.us, p.per, sizeof(E)), pieces(a.dt, a.dts, p.per, sizeof(Td)));
+    if (a.z) p.row_bytes = std::min(p.row_bytes, pieces(a.z, a.zs, p.per, sizeof(E)));
+    p.bc_bytes = std::min(pieces(a.B, a.Bs, a.N, sizeof(E)), pieces(a.C, a.Cs, a.N, sizeof(E)));
     p.y_pairs = p.per % 2 == 0 && aligned(a.y, 2 * sizeof(E));
-    if (a.N <= 4) return launch_scan<E, Td, 1>(p, st);
-    if (a.N <= 8) return launch_scan<E, Td, 2>(p, st);
-    return launch_scan<E, Td, 4>(p, st);
+    if (a.N <= 4) return launch_scan<E, Td, 2, 4>(p, st);
+    if (a.N <= 8) return launch_scan<E, Td, 2, 8>(p, st);
+    return launch_scan<E, Td, 4, 16>(p, st);
 }
 
 // ---- decoding --------------------------------------------------------------

@@ -153,6 +153,9 @@ def test_scan_shapes(ssd, b, T, D, G, N, dtype, dt):
     # few channels: 8 and 16 warps, several rounds, states in blocks and not
     (2, 200, 2400, 1, 20, "bf16"), (1, 200, 2416, 1, 16, "f32"), (1, 300, 40, 1, 64, "bf16"),
     (1, 290, 20, 2, 130, "f32"), (1, 400, 33, 1, 7, "bf16"), (1, 200, 70, 1, 2, "f32"),
+    # very few channels: segments over clusters of 8 and 4, whole and partial ones, states in blocks
+    (1, 1025, 20, 1, 16, "bf16"), (2, 1500, 40, 2, 15, "f32"), (1, 1100, 37, 1, 40, "bf16"), (3, 513, 64, 1, 16, "f32"),
+    (1, 700, 480, 1, 6, "bf16"), (1, 2050, 7, 7, 3, "f32"), (1, 513, 300, 1, 130, "f32"),
     # few channels, few tokens
     (1, 5, 40, 1, 40, "bf16"), (1, 64, 16, 1, 16, "f32"), (1, 63, 16, 1, 17, "f32"),
 ])
@@ -201,10 +204,11 @@ def test_scan_growing_states(ssd):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("off,pad", [(8, 8), (3, 2)])
-def test_scan_slices_of_wider_rows(ssd, dtype, off, pad):
-    """Every input inside wider rows, aligned to 16 bytes and not."""
-    b, T, D, G, N = 2, 70, 24, 2, 16
+@pytest.mark.parametrize("off,pad", [(8, 8), (2, 2), (3, 2)])
+@pytest.mark.parametrize("T,D", [(70, 24), (30, 4800), (270, 24)])
+def test_scan_slices_of_wider_rows(ssd, dtype, off, pad, T, D):
+    """Every input inside wider rows, aligned to 16 bytes, to 4 and to its element."""
+    b, G, N = 2, 2, 16
     d = inputs(b, T, D, G, N, dtype, seed=7)
     dev = cuda(d)
     for k in ("u", "dt", "z", "B", "C"):
@@ -251,6 +255,25 @@ def test_scan_packed_many_channels(ssd):
         y, fin = ssd.ssd_selective_scan_varlen(**cuda(d), cu_seqlens=cu, return_final_states=True)
         check(y, ry, yb, d["u"].dtype)
         check(fin, rh, hb, torch.float32)
+
+
+def test_scan_packed_few_channels(ssd):
+    """Documents over the CTAs of a cluster: long, short, empty and single-token ones, some with
+    segments that hold no token."""
+    cu = [0, 2500, 2501, 2501, 2630, 2900, 3900]
+    for dtype, D, N in (("bf16", 24, 16), ("f32", 17, 20)):
+        d = inputs(1, cu[-1], D, 1, N, dtype, nseq=len(cu) - 1, seed=N)
+        ry, yb, rh, hb = reference(d, cu)
+        y, fin = ssd.ssd_selective_scan_varlen(**cuda(d), cu_seqlens=cu, return_final_states=True)
+        check(y, ry, yb, d["u"].dtype)
+        check(fin, rh, hb, torch.float32)
+    wild = torch.tensor([-7, 2000, 1200, 3905, 800], dtype=torch.int32, device="cuda")
+    guard = torch.full((3900 + 64, 17), 3.0, device="cuda")
+    dev = cuda(d)
+    dev["initial_states"] = dev["initial_states"][:4].contiguous()
+    ssd.ssd_selective_scan_varlen(**dev, cu_seqlens=wild, y=guard[32:32 + 3900][None])
+    torch.cuda.synchronize()
+    assert bool((guard[:32] == 3).all()) and bool((guard[32 + 3900:] == 3).all())
 
 
 def test_scan_rows_behind_the_last_document_stay(ssd):
