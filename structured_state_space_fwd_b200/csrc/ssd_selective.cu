@@ -140,16 +140,19 @@ __device__ __forceinline__ void stage(E* dst, const E* src, int row, int rows, i
             if (K * P4 % 32 == 0 || k < K) copy4(dst + k * W + c, ok ? src + ((int64_t)k * row + c) : src, ok);
         }
     } else {
-        constexpr int kN = (K * W + 31) / 32;
-        E v[kN];                                          // all loads before the first store
+        constexpr int kN = (K * W + 31) / 32, kAtOnce = kN < 4 ? kN : 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kN; i0 += kAtOnce) {
+            E v[kAtOnce];                                 // loads before the first store
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-            const int k = (lane + 32 * i) / W, c = (lane + 32 * i) % W;
-            v[i] = k < rows && c < cols ? src[(int64_t)k * row + c] : E(0.f);
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int k = (lane + 32 * (i0 + i)) / W, c = (lane + 32 * (i0 + i)) % W;
+                v[i] = k < rows && c < cols ? src[(int64_t)k * row + c] : E(0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (K * W % (32 * kAtOnce) == 0 || lane + 32 * (i0 + i) < K * W) dst[lane + 32 * (i0 + i)] = v[i];
         }
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-            if (K * W % 32 == 0 || lane + 32 * i < K * W) dst[lane + 32 * i] = v[i];
     }
 }
 
@@ -445,13 +448,14 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
 // channels a lane halve the reads of B and C), and the lanes' parts of y are summed by exchanges that
 // leave every lane kCutTok / SL tokens.
 //
-// The W warps of a CTA take consecutive runs of kCutTok tokens of the same channels. Each runs from a
-// state of zero and keeps, per token and state, C_t times the product of its decays so far. The
-// entering states go from warp to warp as a chain, h <- (prod a) h + h_local, over shared memory and
-// a named barrier of the two warps, so that the warps stay at different phases; with its entering
-// state a warp adds sum_n (C_t prod a)[n] h[n] to each y_t, at two packed operations per pair of
-// states and no second exponential. 16384 tokens of 2048 channels, 16 states, fp32: 8 warps 526 us,
-// 16 warps 379 (no cut: 1308).
+// The W = kCutWarps warps of a CTA take consecutive runs of kCutTok tokens of the same channels. Each
+// runs from a state of zero and keeps, per token and state, C_t times the product of its decays so far
+// (128 registers: one CTA an SM, which is faster than twice the warps with half the tokens each: 2048
+// tokens of 2048 channels, 16 states, bf16 54 us for 63, 64 states in 8 groups 161 for 177; 16384 tokens
+// in fp32 384 for 378). The entering states go from warp to warp as a chain, h <- (prod a) h + h_local,
+// over shared memory and a named barrier of the two warps, so that the warps stay at different phases;
+// with its entering state a warp adds sum_n (C_t prod a)[n] h[n] to each y_t, at two packed operations
+// per pair of states and no second exponential.
 //
 // kSegments: with so few channels that most SMs would stay empty, a cluster of CTAs shares a unit's
 // tokens, a segment each. Every CTA first runs its segment from a state of zero, without outputs, to
@@ -459,7 +463,7 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
 // the cluster each folds the segments before its own, over distributed shared memory, into its
 // entering states, and runs its segment again with outputs. The exponentials are computed twice, on
 // SMs that had none.
-constexpr int kCutTok = 8;       // 8 floats a token and lane are kept
+constexpr int kCutTok = 16, kCutWarps = 8;
 
 template <typename E, typename Td, int SL>
 struct CutMem {
@@ -489,9 +493,9 @@ struct States {
     }
 };
 
-template <typename E, typename Td, int SL, int W, bool kSegments>
-__global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_constant__ ScanParams p) {
-    constexpr int K = kCutTok;
+template <typename E, typename Td, int SL, bool kSegments>
+__global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __grid_constant__ ScanParams p) {
+    constexpr int K = kCutTok, W = kCutWarps;
     constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
     using Mem = CutMem<E, Td, SL>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -824,11 +828,12 @@ __global__ void __launch_bounds__(W * 32, 16 / W) cut_scan_kernel(const __grid_c
     if constexpr (kSegments) cluster_wait();             // others read this CTA's shared memory until here
 }
 
-template <typename E, typename Td, int SL, int W, bool kSegments>
+template <typename E, typename Td, int SL, bool kSegments>
 cudaError_t launch_cut(const ScanParams& p, int64_t units, int ranks, cudaStream_t st) {
+    constexpr int W = kCutWarps;
     const size_t shared = W * sizeof(CutMem<E, Td, SL>) + (size_t)(p.nblocks + 2 * W) * 64 * 16 +
                           (kSegments ? (size_t)p.nblocks * 64 * 16 + (2 * W + 1) * 32 * 8 : 0);
-    auto kernel = cut_scan_kernel<E, Td, SL, W, kSegments>;
+    auto kernel = cut_scan_kernel<E, Td, SL, kSegments>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
@@ -854,30 +859,33 @@ cudaError_t launch_scan(ScanParams p, cudaStream_t st) {
     const SelectiveArgs& a = p.a;
     const int64_t cblocks = (p.per + CH - 1) / CH, units = a.nseq * a.G * cblocks;
     const int64_t len = (a.T + (a.cu ? a.nseq : 1) - 1) / (a.cu ? a.nseq : 1);
-    // The cut form's 16 warps fill an SM, so it is for units that one wave takes (2048 tokens, 16 states,
-    // bf16: 2048 channels 58 us cut, 100 uncut; 3200 channels 107 cut, 102 uncut), and for sequences of
-    // a round or more. More states than a lane holds make up for few channels, and the uncut form reads
-    // their B and C a block at a time (64 states: 1024 tokens of 10240 channels 458 us cut, 516 uncut;
-    // 512 tokens of 81920 channels 1537 cut, 1215 uncut).
+    const int64_t tiles = (len + kWideTok - 1) / kWideTok;
+    const int64_t rounds = (len + kCutWarps * kCutTok - 1) / (kCutWarps * kCutTok);
     constexpr int S = NS >= 8 ? 2 : 1;
     if (a.N <= NS) {
-        if (units > 148 || len <= 8 * kCutTok) return launch_wide<E, Td, NS, S, false>(p, st);
+        // A CTA of the cut form fills an SM, so it is for units that one wave takes (2048 tokens, 16
+        // states, bf16: 2048 channels 54 us cut, 100 uncut; 3200 channels 107 cut, 102 uncut), and for
+        // sequences of a few tiles (64 tokens of 5120 channels 14 cut, 8 uncut).
+        if (units > 148 || len <= 64) return launch_wide<E, Td, NS, S, false>(p, st);
     } else if constexpr (SL == 4) {
-        if (units > 6 * 148) return launch_wide<E, Td, NS, S, true>(p, st);
+        // More states than a lane holds make up for few channels, and the uncut form reads their B and C
+        // a block at a time. A round of a wave of the cut form takes about 1.5 times a tile of the uncut
+        // one, whose tiles slow down above 6 units an SM (64 states: 1024 tokens of 10240 channels 418 us
+        // cut, 499 uncut; 512 tokens of 81920 channels 1528 cut, 1186 uncut; 16 tokens of 8192 channels
+        // 43 cut, 17 uncut).
+        const int64_t waves = (units + 147) / 148, full = 6 * 148;
+        if (2 * tiles * std::max(units, full) < 3 * waves * rounds * full)
+            return launch_wide<E, Td, NS, S, true>(p, st);
     }
     p.cblocks = cblocks;
     p.nblocks = (int)((a.N + 4 * SL - 1) / (4 * SL));
-    if (units <= 148 && len > 128) {
-        const int64_t rounds = (len + 16 * kCutTok - 1) / (16 * kCutTok);
-        // Clusters of 8 and 4 such CTAs as long as the GPU has them at once (SMs of one cluster lie
-        // together) and the segments have a round each (15 states, bf16, 6720 tokens of 2 x 16 channels:
-        // 214 us without, 59 with 8; 16 states, 8192 tokens of 512 channels: 218 without, 118 with 4).
-        // Two segments would gain nothing, at 1.6 times the work.
-        if (units <= 12 && rounds >= 8) return launch_cut<E, Td, SL, 16, true>(p, units, 8, st);
-        if (units <= 32 && rounds >= 4) return launch_cut<E, Td, SL, 16, true>(p, units, 4, st);
-        return launch_cut<E, Td, SL, 16, false>(p, units, 1, st);
-    }
-    return launch_cut<E, Td, SL, 8, false>(p, units, 1, st);
+    // Clusters of 8 and 4 such CTAs as long as the GPU has them at once (the SMs of a cluster lie
+    // together) and the segments have a round each (15 states, bf16, 6720 tokens of 2 x 16 channels:
+    // 258 us without, 61 with 8; 16 states, 8192 tokens of 512 channels: 200 without, 88 with 4). Two
+    // segments would gain nothing, at 1.6 times the work.
+    if (units <= 12 && rounds >= 8) return launch_cut<E, Td, SL, true>(p, units, 8, st);
+    if (units <= 32 && rounds >= 4) return launch_cut<E, Td, SL, true>(p, units, 4, st);
+    return launch_cut<E, Td, SL, false>(p, units, 1, st);
 }
 
 template <typename E, typename Td>

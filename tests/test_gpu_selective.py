@@ -150,14 +150,15 @@ def test_scan_shapes(ssd, b, T, D, G, N, dtype, dt):
     (1, 65, 19300, 1, 4, "f32"), (2, 17, 9664, 1, 3, "bf16"), (1, 50, 4800, 150, 13, "bf16"),
     # many channels and more states than a lane holds at once
     (4, 140, 4800, 1, 17, "bf16"), (8, 131, 2400, 1, 35, "f32"),
-    # few channels: 8 and 16 warps, several rounds, states in blocks and not
+    # few channels: several rounds of 128 tokens, states in blocks and not
     (2, 200, 2400, 1, 20, "bf16"), (1, 200, 2416, 1, 16, "f32"), (1, 300, 40, 1, 64, "bf16"),
     (1, 290, 20, 2, 130, "f32"), (1, 400, 33, 1, 7, "bf16"), (1, 200, 70, 1, 2, "f32"),
     # very few channels: segments over clusters of 8 and 4, whole and partial ones, states in blocks
     (1, 1025, 20, 1, 16, "bf16"), (2, 1500, 40, 2, 15, "f32"), (1, 1100, 37, 1, 40, "bf16"), (3, 513, 64, 1, 16, "f32"),
     (1, 700, 480, 1, 6, "bf16"), (1, 2050, 7, 7, 3, "f32"), (1, 513, 300, 1, 130, "f32"),
     # few channels, few tokens
-    (1, 5, 40, 1, 40, "bf16"), (1, 64, 16, 1, 16, "f32"), (1, 63, 16, 1, 17, "f32"),
+    (1, 5, 40, 1, 40, "bf16"), (1, 64, 16, 1, 16, "f32"), (1, 63, 16, 1, 17, "f32"), (2, 16, 4096, 1, 20, "bf16"),
+    (1, 65, 40, 1, 16, "bf16"), (1, 128, 33, 1, 5, "f32"), (1, 129, 2368, 1, 16, "bf16"), (1, 40, 2384, 1, 33, "f32"),
 ])
 def test_scan_forms(ssd, b, T, D, G, N, dtype):
     """Sizes on both sides of every choice between the kernels' forms."""
