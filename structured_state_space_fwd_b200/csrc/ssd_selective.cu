@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, kBlocks ? 9 : 6) wide_scan_ke
                     quad_of(Ct + k * NS + 2 * i, Cv[k & 1] + i);
                 }
 #pragma unroll
-                for (int i = 0; i < P; ++i) e[k & 1][i] = ex2(mul_(both(st), A[i]));
+                for (int i = 0; i < P; ++i) e[k & 1][i] = decay_of(both(st), A[i]);
             };
             float part[2 * S];                               // of y, for S pairs of tokens
             prepare(0);
@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) to[c][i] = ex2(mul_(both(c ? s.z : s.x), A.v[c][i]));
+                            for (int i = 0; i < 2; ++i) to[c][i] = decay_of(both(c ? s.z : s.x), A.v[c][i]);
                     };
                     exps(e[0], sk);
 #pragma unroll
@@ -1065,7 +1065,7 @@ __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
                 Cv[r][k].widen(Cf);
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    h[r][k][m] = fma_(ex2(mul_(A[k][m], all<F>(dtr))), h[r][k][m], mul_(Bf[m], all<F>(du)));
+                    h[r][k][m] = fma_(decay_of(A[k][m], all<F>(dtr)), h[r][k][m], mul_(Bf[m], all<F>(du)));
                     sum = fma_(Cf[m], h[r][k][m], sum);
                 }
             }

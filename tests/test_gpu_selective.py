@@ -197,6 +197,19 @@ def test_scan_fast_and_slow_decays(ssd, N):
     run_and_check(ssd, d)
 
 
+@pytest.mark.parametrize("T,D", [(1, 40), (50, 40), (300, 40), (1200, 40), (33, 4800)])
+def test_steps_of_zero_leave_the_state(ssd, T, D):
+    """dt = 0: a decay of exactly 1 and nothing added, in every form."""
+    d = cuda(inputs(1, T, D, 1, 16, "f32", seed=1, softplus=False))
+    d["dt"].zero_()
+    _, fin = ssd.ssd_selective_scan(**d, return_final_states=True)
+    assert torch.equal(fin, d["initial_states"])
+    state = d.pop("initial_states")
+    before = state.clone()
+    ssd.ssd_selective_step(**d, state=state)
+    assert torch.equal(state, before)
+
+
 def test_scan_growing_states(ssd):
     """A above 0 is not refused: states grow, within fp32's range."""
     d = inputs(1, 90, 16, 1, 16, "f32", seed=2, softplus=False)
