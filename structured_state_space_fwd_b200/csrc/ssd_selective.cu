@@ -914,7 +914,8 @@ cudaError_t scan_any(const SelectiveArgs& a, cudaStream_t st) {
 // channel in registers for all of the call's tokens, so that A (as large as one row's state) is read
 // once for them and their loads are in flight together. What a (row, channel) needs once - the step,
 // dt u, the gate - is computed by one of the L lanes and handed to the others; the rows' sums are
-// exchanged so that each row ends in the lane that holds its u and gate.
+// exchanged so that each row ends in the lane that holds its u and gate. 128 sequences of 5120 channels,
+// 16 states: 20 us for 90 MB (0.68 of the copy rate); all lanes computing the scalars 39 us.
 constexpr int kStepThreads = 128;
 
 struct StepParams {
