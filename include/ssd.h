@@ -421,8 +421,9 @@ typedef struct {
 /*
  * Whole prompts.
  *   u, dt, z           [b, T, D], strides as given; z NULL: no gate.
- *   A                  [D, N] fp32 (not checked for sign; a decay above 1 that
- *                      overflows fp32 gives inf or NaN).
+ *   A                  [D, N] fp32 (not checked for sign; where the decays' product
+ *                      over a stretch of tokens overflows fp32 the result can be
+ *                      inf or NaN).
  *   B, C               [b, T, G, N], strides as given ([G, N] contiguous).
  *   D, dt_bias         [D] fp32 or NULL (0).
  *   initial_states     [b, D, N] fp32 or NULL (zeros).

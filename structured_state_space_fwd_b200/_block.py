@@ -4,7 +4,8 @@ it, and the selective scan with a diagonal A. Argument marshalling only.
 Inputs may be slices of wider rows (a projection's output): channels contiguous,
 any non-negative strides of tokens and batch rows. Outputs are contiguous. Every
 tensor is on one device, whichever is current; a call runs on that device's
-current stream unless `stream` is given.
+current stream, or on `stream`, which the caller orders behind the work that made
+the inputs (new outputs come from the current stream's memory).
 """
 from __future__ import annotations
 
@@ -108,8 +109,9 @@ def _call(name, t, stream, *args):
         check(st, name)
 
 
-def _offsets(cu_seqlens, T, device):
-    """Device offsets of a pack: a device int32 tensor as is, a host list checked and copied."""
+def _offsets(cu_seqlens, T, device, stream=None):
+    """Device offsets of a pack: a device int32 tensor as is, a host list checked and copied. The
+    copy is made, and its memory used again, in the order of the stream that reads it."""
     if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.is_cuda:
         if (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous()
                 or cu_seqlens.numel() < 1):
@@ -120,7 +122,11 @@ def _offsets(cu_seqlens, T, device):
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
     from . import check_cu_seqlens
-    return torch.tensor(check_cu_seqlens(cu_seqlens, T), dtype=torch.int32).to(device)
+    cu = torch.tensor(check_cu_seqlens(cu_seqlens, T), dtype=torch.int32)
+    if stream is None:
+        return cu.to(device)
+    with torch.cuda.stream(stream):
+        return cu.to(device)
 
 
 # ---- the short causal convolution ------------------------------------------
@@ -213,7 +219,7 @@ def ssd_causal_conv1d_varlen(u, weight, bias=None, cu_seqlens=None, silu: bool =
     W, shape, ys, yp = _conv_args(u, weight, bias, silu, split, out)
     if u.shape[0] != 1:
         raise ValueError("packed documents need batch 1 (u [1, T, C])")
-    cu = _offsets(cu_seqlens, u.shape[1], u.device)
+    cu = _offsets(cu_seqlens, u.shape[1], u.device, stream)
     n = cu.numel() - 1
     fin = _conv_states(u, W, n, initial_states, return_final_states, final_states)
     _call("ssd_causal_conv1d_varlen", u, stream, shape, u.data_ptr(), weight.data_ptr(),
@@ -341,7 +347,7 @@ def ssd_selective_scan_varlen(u, dt, A, B, C, D=None, z=None, dt_bias=None, dt_s
     N, shape, ins, y = _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y)
     if u.shape[0] != 1:
         raise ValueError("packed documents need batch 1 (u [1, T, D])")
-    cu = _offsets(cu_seqlens, u.shape[1], u.device)
+    cu = _offsets(cu_seqlens, u.shape[1], u.device, stream)
     n = cu.numel() - 1
     fin = _selective_states(u, n, N, initial_states, return_final_states, final_states)
     _call("ssd_selective_scan_varlen", u, stream, shape, *ins, cu.data_ptr(), n,

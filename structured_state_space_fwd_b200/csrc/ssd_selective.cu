@@ -14,8 +14,8 @@
 // is cut, and what is left is moved off the inner loop.
 //
 // Two forms, both with their inputs copied asynchronously a tile ahead:
-//   many channels (wide_scan_kernel): a lane holds the states of a channel, nothing is exchanged
-//     between lanes, and two warps take the tiles of a block of channels in turn;
+//   many channels (wide_scan_kernel): one or two lanes hold the states of a channel, and two warps
+//     take the tiles of a block of channels in turn;
 //   few channels (cut_scan_kernel): lanes share pairs of channels, and the warps of a CTA take
 //     consecutive runs of tokens of the same channels; for very few, the CTAs of a cluster take
 //     consecutive segments.
@@ -30,7 +30,6 @@
 
 namespace ssd {
 namespace {
-
 
 struct ScanParams {
     SelectiveArgs a;
@@ -63,17 +62,16 @@ __device__ __forceinline__ void pair_arrive(int id) {
 #define SSD_ARRIVE(i) \
     if constexpr (i < kIds) { if (id == i) asm volatile("bar.arrive " #i ", 64;" ::: "memory"); }
     SSD_ARRIVE(0) SSD_ARRIVE(1) SSD_ARRIVE(2) SSD_ARRIVE(3) SSD_ARRIVE(4) SSD_ARRIVE(5) SSD_ARRIVE(6) SSD_ARRIVE(7)
-    SSD_ARRIVE(8) SSD_ARRIVE(9) SSD_ARRIVE(10) SSD_ARRIVE(11) SSD_ARRIVE(12) SSD_ARRIVE(13) SSD_ARRIVE(14)
-    SSD_ARRIVE(15)
 #undef SSD_ARRIVE
+    static_assert(kIds <= 8, "");
 }
 template <int kIds>
 __device__ __forceinline__ void pair_wait(int id) {
 #define SSD_WAIT(i) \
     if constexpr (i < kIds) { if (id == i) asm volatile("bar.sync " #i ", 64;" ::: "memory"); }
     SSD_WAIT(0) SSD_WAIT(1) SSD_WAIT(2) SSD_WAIT(3) SSD_WAIT(4) SSD_WAIT(5) SSD_WAIT(6) SSD_WAIT(7)
-    SSD_WAIT(8) SSD_WAIT(9) SSD_WAIT(10) SSD_WAIT(11) SSD_WAIT(12) SSD_WAIT(13) SSD_WAIT(14) SSD_WAIT(15)
 #undef SSD_WAIT
+    static_assert(kIds <= 8, "");
 }
 
 // The CTAs of a cluster: rank, a barrier in two halves, and loads from another CTA's shared memory.
@@ -602,11 +600,10 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
             const float2 lo = add_(up ? v[2] : v[0], give(up ? v[0] : v[2], 2 * CL));
             const float2 hi = add_(up ? v[3] : v[1], give(up ? v[1] : v[3], 2 * CL));
             r = add_(odd ? hi : lo, give(odd ? lo : hi, CL));
-        } else if constexpr (SL == 2) {
+        } else {
+            static_assert(SL == 2 || SL == 4, "");
             const bool odd = j & 1;
             r = add_(odd ? v[1] : v[0], give(odd ? v[0] : v[1], CL));
-        } else {
-            r = v[0];
         }
         ysum[q] = add_(ysum[q], r);
     };
@@ -664,7 +661,7 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
                 }
                 States h, decay;
                 float2 steps = both(0.f);                    // sum of the tile's
-                float2 gc[K][2][2];               // C_t times the decays up to t
+                float2 gc[K][2][2];                          // C_t times the decays up to t
                 decay.fill(1.f);
                 h.fill(0.f);
                 if (n > 0) {

@@ -480,6 +480,15 @@ def test_scan_streams_and_graphs(ssd):
     b = ssd.ssd_selective_scan(**d)
     torch.cuda.synchronize()
     assert torch.equal(a, ref) and torch.equal(b, ref)
+    one = {k: (v[:1] if isinstance(v, torch.Tensor) and v.dim() > 2 else v) for k, v in d.items()}
+    one["initial_states"] = d["initial_states"].contiguous()
+    packed = ssd.ssd_selective_scan_varlen(**one, cu_seqlens=[0, 17, 40])
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):                          # host offsets: copied and freed on the stream that reads them
+        c = ssd.ssd_selective_scan_varlen(**one, cu_seqlens=[0, 17, 40], stream=side)
+        torch.zeros(64, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(c, packed)
     init = d.pop("initial_states")
     state, out = init.clone(), torch.empty_like(ref[:, :1])
     tok = {k: d[k][:, :1].clone() for k in ("u", "dt", "B", "C", "z")}
