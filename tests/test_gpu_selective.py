@@ -263,8 +263,8 @@ def test_scan_packed(ssd, cu, dtype, D, N):
 def test_scan_packed_many_channels(ssd):
     """Documents of every length around a tile, many of them, in the form for many channels."""
     cu = [0, 1, 1, 17, 33, 48, 49, 81, 112, 113, 145, 177, 178]
-    for dtype, N in (("bf16", 16), ("f32", 20)):
-        d = inputs(1, cu[-1], 1600 if N == 16 else 1700, 1, N, dtype, nseq=len(cu) - 1, seed=N)
+    for dtype, N, D in (("bf16", 16, 1600), ("f32", 20, 1700), ("f32", 16, 1700), ("bf16", 18, 400)):
+        d = inputs(1, cu[-1], D, 1, N, dtype, nseq=len(cu) - 1, seed=N)
         ry, yb, rh, hb = reference(d, cu)
         y, fin = ssd.ssd_selective_scan_varlen(**cuda(d), cu_seqlens=cu, return_final_states=True)
         check(y, ry, yb, d["u"].dtype)
