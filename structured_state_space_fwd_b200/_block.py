@@ -74,6 +74,11 @@ def _first(t, name, dim):
         raise ValueError(f"{name} must have {dim} dimensions, got {t.dim()}")
 
 
+def _like(u):
+    """A new contiguous tensor of u's shape and type."""
+    return torch.empty_like(u) if u.is_contiguous() else u.new_empty(u.shape)
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else None
 
@@ -162,7 +167,7 @@ def _conv_args(u, weight, bias, silu, split, out):
     if not 1 <= len(sizes) <= 3 or min(sizes) < 0 or sum(sizes) != C:
         raise ValueError(f"split must be up to three sizes that add up to {C}, got {split}")
     if out is None:
-        ys = [u.new_empty((b, T, c)) for c in sizes]
+        ys = [_like(u)] if len(sizes) == 1 else [u.new_empty((b, T, c)) for c in sizes]
     else:
         ys = [out] if split is None else list(out)
         if len(ys) != len(sizes):
@@ -300,7 +305,7 @@ def _selective_args(u, dt, A, B, C, D, z, dt_bias, dt_softplus, y):
         us, ds, bs, cs = u.stride(), dt.stride(), B.stride(), C.stride()
         zs = (0, 0) if z is None else z.stride()
     if y is None:
-        y = u.new_empty(size)
+        y = _like(u)
     else:
         _whole(y, "y", size, dtype, u.device)
     shape = _selective_shape(b, T, Dc, G, N, us[0], us[1], ds[0], ds[1], zs[0], zs[1], bs[0], bs[1], cs[0], cs[1],
