@@ -241,9 +241,10 @@ __device__ __forceinline__ float2 tokens_of(const E (*rows)[CH], int k, int ch) 
 }
 
 // S: lanes of a channel, each with NS / S of the states and every S-th pair of tokens to prepare and
-// finish. kBlocks: more states than NS, which the inner loops then take a block at a time.
-template <typename E, typename Td, int NS, int S, bool kBlocks>
-__global__ void __launch_bounds__(kWideWarps * 32, kBlocks ? 9 : 6) wide_scan_kernel(const __grid_constant__ ScanParams p) {
+// finish. kBlocks: more states than NS, which the inner loops then take a block at a time. kCtas: CTAs an
+// SM that the registers are capped for.
+template <typename E, typename Td, int NS, int S, bool kBlocks, int kCtas>
+__global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kWideTok, P = NS / S / 2, W = kWideWarps, CH = 32 / S, Q = K / 2 / S;
     using Mem = WideMem<E, Td, NS, S>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -454,7 +455,12 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const size_t shared = kWideWarps * sizeof(WideMem<E, Td, NS, S>) +
                           (size_t)p.nblocks * (NS / S) * 32 * 4 * (p.nblocks > 1 ? 2 : 1);
-    auto kernel = wide_scan_kernel<E, Td, NS, S, kBlocks>;
+    // 6 CTAs an SM (168 registers), or 8 where that saves a wave (1024 tokens, 16 states, bf16: 960 units 132
+    // us with 8, 140 with 6; 800 units 105 and 101). Blocks of states gain from warps instead (9).
+    auto kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, kBlocks ? 9 : 6>;
+    if constexpr (!kBlocks)
+        if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
+            kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, 8>;
     if (shared > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
         if (e != cudaSuccess) return e;
