@@ -15,7 +15,6 @@ using ssd::aligned;
 using ssd::overlaps;
 using ssd::Range;
 
-constexpr int64_t kMaxState = 256;
 constexpr int64_t kMaxDocs = 1 << 24;
 constexpr int64_t kMaxTokens = 0x7fff0000;   // tokens and rows of the scan's kernels are 32-bit
 constexpr int64_t kMaxRow = 0x7fffffff;      // numbers, so that an offset is one 32 x 32 product
@@ -121,7 +120,7 @@ ssd_status_t check_selective_shape(const ssd_selective_shape_t* s) {
     if (!dtype_ok(s->dtype) || !dtype_ok(s->dt_dtype) || (s->dt_dtype != SSD_F32 && s->dt_dtype != s->dtype) ||
         (s->dt_softplus != 0 && s->dt_softplus != 1))
         return SSD_ERR_INVALID_ARG;
-    if (s->dstate > kMaxState || s->seqlen > kMaxTokens) return SSD_ERR_UNSUPPORTED;
+    if (s->dstate > ssd::kMaxSelectiveStates || s->seqlen > kMaxTokens) return SSD_ERR_UNSUPPORTED;
     if ((double)s->batch * (double)s->seqlen * (double)s->channels > kMaxElems ||
         (double)s->batch * (double)s->seqlen * (double)s->ngroups * (double)s->dstate > kMaxElems ||
         (double)s->batch * (double)s->channels * (double)s->dstate > kMaxElems)

@@ -175,6 +175,7 @@ struct SelectiveArgs {
     void* y;
     float* fin;                // [nseq, D, N] or null
 };
+constexpr int64_t kMaxSelectiveStates = 256;    // N
 cudaError_t launch_selective_scan(const SelectiveArgs& a, cudaStream_t st);
 cudaError_t launch_selective_step(const SelectiveArgs& a, cudaStream_t st);
 
@@ -189,6 +190,15 @@ inline bool overlaps(Range a, Range b) {
     return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
 }
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// Lets a kernel take up to `most` bytes of dynamic shared memory a launch. The limit belongs to the
+// function, not to the call: `most` is the same for every call of a kernel (the largest that any needs),
+// so that no host thread lowers it between another's setting and its launch.
+template <typename K>
+cudaError_t allow_shared(K* kernel, size_t most) {
+    if (most <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
 
 // Sets the message ssd_last_error_detail() returns on the calling host thread.
 void set_error_detail(const char* msg);

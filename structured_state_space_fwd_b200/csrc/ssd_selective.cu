@@ -453,18 +453,18 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     p.nblocks = (int)((a.N + NS - 1) / NS);
     const int64_t units = a.nseq * a.G * p.cblocks;
     if (units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t shared = kWideWarps * sizeof(WideMem<E, Td, NS, S>) +
-                          (size_t)p.nblocks * (NS / S) * 32 * 4 * (p.nblocks > 1 ? 2 : 1);
+    auto bytes = [](size_t nblocks) {
+        return kWideWarps * sizeof(WideMem<E, Td, NS, S>) + nblocks * (NS / S) * 32 * 4 * (kBlocks ? 2 : 1);
+    };
+    const size_t shared = bytes(p.nblocks);
     // 6 CTAs an SM (168 registers), or 8 where that saves a wave (1024 tokens, 16 states, bf16: 960 units 132
     // us with 8, 140 with 6; 800 units 105 and 101). Blocks of states gain from warps instead (9).
     auto kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, kBlocks ? 9 : 6>;
     if constexpr (!kBlocks)
         if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
             kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, 8>;
-    if (shared > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(kernel, bytes(kBlocks ? kMaxSelectiveStates / NS : 1));
+    if (e != cudaSuccess) return e;
     // Over one to five waves of 6 CTAs an SM the order decides the tail (8192 tokens of 2048 channels in 16
     // documents 134 us ranked, 176 in the pack's order); with more, short documents are better spread
     // between long ones (64 documents 166 ranked, 150 not).
@@ -864,13 +864,16 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
 template <typename E, typename Td, int SL, bool kSegments>
 cudaError_t launch_cut(ScanParams p, int64_t units, int ranks, cudaStream_t st) {
     constexpr int W = kCutWarps;
-    const size_t shared = W * sizeof(CutMem<E, Td, SL>) + (size_t)(p.nblocks + 2 * W) * 64 * 16 +
-                          (kSegments ? (size_t)p.nblocks * 64 * 16 + (2 * W + 1) * 32 * 8 : 0);
+    constexpr auto bytes = [](size_t nblocks) {
+        return W * sizeof(CutMem<E, Td, SL>) + (nblocks + 2 * W) * 64 * 16 +
+               (kSegments ? nblocks * 64 * 16 + (2 * W + 1) * 32 * 8 : 0);
+    };
+    const size_t shared = bytes(p.nblocks);
+    constexpr size_t most = bytes(SL == 4 ? kMaxSelectiveStates / 16 : 1);     // two lanes: up to 8 states
+    static_assert(most <= 227 * 1024, "");
     auto kernel = cut_scan_kernel<E, Td, SL, kSegments>;
-    if (shared > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_shared(kernel, most);
+    if (e != cudaSuccess) return e;
     p.ranked = p.a.cu && p.a.nseq <= kRanked && units > 148 && units <= 5 * 148;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
