@@ -275,8 +275,10 @@ __global__ void __launch_bounds__(256) chunk_scan_simt_kernel(
     }
 }
 
-inline size_t chunk_scan_smem(const Dims& d) {
-    return sizeof(float) * (size_t)(2 * 32 * (d.N + 1) + 32 * (d.P + 1) + d.P * 33 + 32 * 33 + 64);
+constexpr int64_t kMaxDim = 256;    // of P and N
+
+constexpr size_t chunk_scan_smem(int64_t P, int64_t N) {
+    return sizeof(float) * (size_t)(2 * 32 * (N + 1) + 32 * (P + 1) + P * 33 + 32 * 33 + 64);
 }
 
 }  // namespace
@@ -286,9 +288,7 @@ cudaError_t launch_chunk_cumsum(const Dims& d, const float* dt, const float* A, 
     if (d.b == 0 || d.nc == 0) return cudaSuccess;
     dim3 grid((unsigned)d.nc, (unsigned)((d.H + 31) / 32), (unsigned)d.b);
     size_t smem = sizeof(float) * (size_t)d.Q * 33;
-    cudaError_t e = cudaFuncSetAttribute(chunk_cumsum_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    // a chunk has at most 256 tokens: within what any kernel may take
     chunk_cumsum_kernel<<<grid, 256, smem, st>>>(dt, A, cs, d.T, d.H, (int)d.Q, d.nc);
     return cudaGetLastError();
 }
@@ -333,18 +333,18 @@ cudaError_t launch_chunk_scan_simt(const Dims& d, const void* x, const float* dt
                                    const float* entry, void* y, cudaStream_t st) {
     if (d.b == 0 || d.nc == 0) return cudaSuccess;
     dim3 grid((unsigned)((d.Q + 31) / 32), (unsigned)(d.nc * d.H), (unsigned)d.b);
-    const size_t smem = chunk_scan_smem(d);
+    const size_t smem = chunk_scan_smem(d.P, d.N);
     cudaError_t e;
     if (d.dtype == SSD_BF16) {
         auto k = chunk_scan_simt_kernel<__nv_bfloat16, false>;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_shared(k, chunk_scan_smem(kMaxDim, kMaxDim));
         if (e != cudaSuccess) return e;
         k<<<grid, 256, smem, st>>>((const __nv_bfloat16*)x, dt, (const __nv_bfloat16*)B,
                                    (const __nv_bfloat16*)C, D, cs, entry, (__nv_bfloat16*)y, d.T,
                                    d.H, d.P, d.G, d.N, (int)d.Q, d.nc);
     } else {
         auto k = chunk_scan_simt_kernel<float, true>;
-        e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        e = allow_shared(k, chunk_scan_smem(kMaxDim, kMaxDim));
         if (e != cudaSuccess) return e;
         k<<<grid, 256, smem, st>>>((const float*)x, dt, (const float*)B, (const float*)C, D, cs,
                                    entry, (float*)y, d.T, d.H, d.P, d.G, d.N, (int)d.Q, d.nc);

@@ -1,5 +1,6 @@
 """Calls on several host threads are independent: threads that call one kernel with different amounts of
 shared memory at the same time each get what they get alone."""
+import ctypes
 import threading
 
 import pytest
@@ -72,3 +73,30 @@ def test_selective_scan(ssd, monkeypatch, T, D, dtype, few, many):
     assert together(calls) == []
     for _, y, fin, _, expect in kept:
         assert torch.equal(y, expect[0]) and torch.equal(fin, expect[1])
+
+
+def test_chunk_steps(ssd):
+    """The cumulative sums and the scan of a chunk in fp32, with the smallest and the largest chunks and states."""
+    calls, kept = [], []
+    for Q, P, N in ((16, 4, 4), (256, 256, 256)) * 2:
+        b, T, H = 1, Q, 1
+        shape = ssd.ShapeT(b, T, H, P, 1, N, Q, 0, 0)
+        g = torch.Generator().manual_seed(Q)
+
+        def new(*s):
+            return torch.randn(*s, generator=g).cuda()
+        x, dt, A, B, C = new(b, T, H, P), new(b, T, H).abs() * 0.1, -new(H).abs(), new(b, T, 1, N), new(b, T, 1, N)
+        cs = ssd.ssd_chunk_cumsum(dt, A, Q, shape)
+        entry = new(b, 1, H, P, N)
+        y = ssd.ssd_chunk_scan(x, dt, B, C, None, cs, entry, shape)
+        cs1, y1, stream = torch.zeros_like(cs), torch.zeros_like(y), torch.cuda.Stream()
+        p = [t.data_ptr() for t in (x, dt, B, C)]
+        lib, ref = ssd.lib(), ctypes.byref(shape)
+        calls.append((lib.ssd_chunk_cumsum, (ref, p[1], A.data_ptr(), cs1.data_ptr(), stream.cuda_stream)))
+        calls.append((lib.ssd_chunk_scan, (ref, *p, None, cs.data_ptr(), entry.data_ptr(), y1.data_ptr(),
+                                           stream.cuda_stream)))
+        kept.append((x, dt, A, B, C, cs, entry, y, cs1, y1, stream, shape))
+    torch.cuda.synchronize()
+    assert together(calls) == []
+    for *_, cs, entry, y, cs1, y1, stream, shape in kept:
+        assert torch.equal(cs, cs1) and torch.equal(y, y1)
