@@ -410,8 +410,10 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
             for (int i = 0; i < P; ++i) carry[(nb * P + i) * 32] = h[i];
         }
         if (it + 1 < tiles) pair_arrive<W>(warp ^ 1);
+        if (a.Dskip) {                                       // 0 times an infinite u would be NaN
 #pragma unroll
-        for (int q = 0; q < Q; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
+            for (int q = 0; q < Q; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
+        }
         if (zb) {
 #pragma unroll
             for (int q = 0; q < Q; ++q) yv[q] = mul_(yv[q], silu(tokens_of(m.z[sr], 2 * (q * S + j), ch)));
@@ -794,8 +796,10 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
             if (!kOut || n <= 0) continue;
             E* to = yb + (int64_t)(t + j) * (int)Dr;
             const int64_t step = SL * Dr;
+            if (a.Dskip) {
 #pragma unroll
-            for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+                for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+            }
             if (zb) {
 #pragma unroll
                 for (int q = 0; q < K / SL; ++q) ysum[q] = mul_(ysum[q], silu(pair_of(&m.z[sr][q * SL + j][2 * cp])));
@@ -1133,7 +1137,7 @@ __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
 #pragma unroll
         for (int q = 0; q < Q; ++q)
             if (j < PL && q * PL + own < rows)
-                store_elem(y + q * PL * a.T * a.D, fmaf(skip, u[q], sum[q]) * gate[q]);
+                store_elem(y + q * PL * a.T * a.D, (a.Dskip ? fmaf(skip, u[q], sum[q]) : sum[q]) * gate[q]);
     }
     float* s = state;
 #pragma unroll
