@@ -200,6 +200,64 @@ __device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2* v) {
     v[1] = make_float2(bf16_lo(q.y), bf16_hi(q.y));
 }
 
+// ---- padded states beside infinities -----------------------------------------
+//
+// The kernels run states from N on, up to their lanes' number, with rates, B and C of 0. They stay 0 as
+// long as the steps and their products with u are finite; 0 times an infinity is NaN, stays NaN to the
+// end of the sequence, and reaches y, which may be infinite instead. So where the last padded state is not
+// 0 at the end, each warp goes over the y that it stored: where that is NaN, the sum over the N states
+// alone takes its place. The kernels' loops have no part in this (checks of every tile's dt u, or of its
+// states, cost 3 to 20 %; this up to 10, 2 on average). Where there is no D, 0 times an infinite u may not be
+// added either. kCare, of the kernels: the call has padded states or no D; else there is nothing to look after.
+//
+// Warp w has stored the tiles of kTok tokens w, w + kWarps, .. from token `from` on to `end`; the sequence
+// starts at t0. which: bits of the channels; owner(k, c): the lane that stored token k of a tile. A lane has
+// the states lane + 32 i, one token after another.
+template <int kTok, int kWarps, typename E, typename Td, typename Owner>
+__device__ __noinline__ void sum_again(const ScanParams& p, int64_t seq, int64_t g, int64_t d0, int t0, int from,
+                                       int end, unsigned which, Owner owner) {
+    const SelectiveArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, N = (int)a.N;
+    const int64_t b = a.cu ? 0 : seq;
+#pragma unroll 1
+    for (; which; which &= which - 1) {
+        const int c = __ffs(which) - 1;
+        const int64_t d = d0 + c;
+        const float skip = a.Dskip ? a.Dskip[d] : 0.f, bias = a.dt_bias ? a.dt_bias[d] : 0.f;
+        float h[kMaxSelectiveStates / 32];
+#pragma unroll 1
+        for (int i = 0; i * 32 + lane < N; ++i) h[i] = a.init ? a.init[(seq * a.D + d) * N + i * 32 + lane] : 0.f;
+#pragma unroll 1
+        for (int t = t0; t < end; ++t) {
+            float dt = to_float(static_cast<const Td*>(a.dt)[b * a.dts.batch + (int64_t)t * a.dts.row + d]) + bias;
+            if (a.softplus) dt = softplus(dt);
+            const float u = to_float(static_cast<const E*>(a.u)[b * a.us.batch + (int64_t)t * a.us.row + d]);
+            const E* const B = static_cast<const E*>(a.B) + b * a.Bs.batch + (int64_t)t * a.Bs.row + g * N;
+            const E* const C = static_cast<const E*>(a.C) + b * a.Cs.batch + (int64_t)t * a.Cs.row + g * N;
+            float sum = 0.f;
+            bool lost = false;
+#pragma unroll 1
+            for (int i = 0; i * 32 + lane < N; ++i) {
+                const int n = i * 32 + lane;
+                h[i] = fmaf(decay_of(dt, a.A[d * N + n] * kLog2e), h[i], dt * u * to_float(B[n]));
+                sum = fmaf(to_float(C[n]), h[i], sum);
+                lost |= h[i] != h[i];
+            }
+            __syncwarp();
+            if (__any_sync(0xffffffffu, lost)) break;        // a state that is NaN stays it, and y with it
+#pragma unroll
+            for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            const int k = t - from;
+            if (k < 0 || k / kTok % kWarps != warp || owner(k % kTok, c) != lane) continue;
+            E* const y = static_cast<E*>(a.y) + (b * a.T + t) * a.D + d;
+            if (to_float(*y) == to_float(*y)) continue;
+            if (a.Dskip) sum = fmaf(skip, u, sum);
+            if (a.z) sum *= silu(to_float(static_cast<const E*>(a.z)[b * a.zs.batch + (int64_t)t * a.zs.row + d]));
+            store_elem(y, sum);
+        }
+    }
+}
+
 // ---- many channels -----------------------------------------------------------
 //
 // S = 2 lanes (1 with up to 4 states) hold a channel's states, 8 each of 16 at a time, and every
@@ -243,7 +301,7 @@ __device__ __forceinline__ float2 tokens_of(const E (*rows)[CH], int k, int ch) 
 // S: lanes of a channel, each with NS / S of the states and every S-th pair of tokens to prepare and
 // finish. kBlocks: more states than NS, which the inner loops then take a block at a time. kCtas: CTAs an
 // SM that the registers are capped for.
-template <typename E, typename Td, int NS, int S, bool kBlocks, int kCtas>
+template <typename E, typename Td, int NS, int S, bool kBlocks, bool kCare, int kCtas>
 __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kWideTok, P = NS / S / 2, W = kWideWarps, CH = 32 / S, Q = K / 2 / S;
     using Mem = WideMem<E, Td, NS, S>;
@@ -410,9 +468,10 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
             for (int i = 0; i < P; ++i) carry[(nb * P + i) * 32] = h[i];
         }
         if (it + 1 < tiles) pair_arrive<W>(warp ^ 1);
-        if (a.Dskip) {                                       // 0 times an infinite u would be NaN
 #pragma unroll
-            for (int q = 0; q < Q; ++q) yv[q] = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
+        for (int q = 0; q < Q; ++q) {
+            const float2 with = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
+            yv[q] = !kCare || a.Dskip ? with : yv[q];
         }
         if (zb) {
 #pragma unroll
@@ -435,6 +494,13 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
         }
     }
     copy_wait<0>();
+    if (kCare && N % NS != 0) {
+        asm volatile("bar.sync 2, 64;" ::: "memory");        // (0 and 1 are the warps' own)
+        const bool odd = in && j == S - 1 && carry[(NB * P - 1) * 32].y != 0.f;
+        const unsigned which = __ballot_sync(0xffffffffu, odd) >> ((S - 1) * CH);
+        if (which)
+            sum_again<K, W, E, Td>(p, seq, g, d0, t0, t0, t1, which, [](int k, int c) { return k / 2 % S * CH + c; });
+    }
     // the warp that wrote the carried states last
     if (!a.fin || !in || warp != (tiles == 0 ? 0 : (tiles - 1) % W)) return;
     for (int nb = 0; nb < NB; ++nb) {
@@ -461,10 +527,13 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     const size_t shared = bytes(p.nblocks);
     // 6 CTAs an SM (168 registers), or 8 where that saves a wave (1024 tokens, 16 states, bf16: 960 units 132
     // us with 8, 140 with 6; 800 units 105 and 101). Blocks of states gain from warps instead (9).
-    auto kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, kBlocks ? 9 : 6>;
+    const bool care = a.N % NS != 0 || !a.Dskip;
+    auto kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, kBlocks ? 9 : 6>
+                       : wide_scan_kernel<E, Td, NS, S, kBlocks, false, kBlocks ? 9 : 6>;
     if constexpr (!kBlocks)
         if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
-            kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, 8>;
+            kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, 8>
+                          : wide_scan_kernel<E, Td, NS, S, kBlocks, false, 8>;
     const cudaError_t e = allow_shared(kernel, bytes(kBlocks ? kMaxSelectiveStates / NS : 1));
     if (e != cudaSuccess) return e;
     // Over one to five waves of 6 CTAs an SM the order decides the tail (8192 tokens of 2048 channels in 16
@@ -528,7 +597,7 @@ struct States {
     }
 };
 
-template <typename E, typename Td, int SL, bool kSegments>
+template <typename E, typename Td, int SL, bool kSegments, bool kCare>
 __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kCutTok, W = kCutWarps;
     constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
@@ -559,6 +628,7 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
     }
     // the CTA's segment: whole rounds, as many for each rank but the last ones
     bool last = true;                                    // whether the sequence ends here
+    const int first = t0;                                // of the sequence
     if constexpr (kSegments) {
         const int end = t1, part = (max(t1 - t0, 0) + ranks * W * K - 1) / (ranks * W * K) * (W * K);
         const int64_t from = t0 + (int64_t)rank * part;
@@ -796,9 +866,10 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
             if (!kOut || n <= 0) continue;
             E* to = yb + (int64_t)(t + j) * (int)Dr;
             const int64_t step = SL * Dr;
-            if (a.Dskip) {
 #pragma unroll
-                for (int q = 0; q < K / SL; ++q) ysum[q] = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+            for (int q = 0; q < K / SL; ++q) {
+                const float2 with = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
+                ysum[q] = !kCare || a.Dskip ? with : ysum[q];
             }
             if (zb) {
 #pragma unroll
@@ -846,6 +917,20 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
         cluster_arrive();
     }
     run(std::true_type{}, carry);
+    if (kCare && N % NS != 0) {
+        __syncthreads();
+        States h;
+        h.load(carry + (NB - 1) * 64 + lane);
+        const unsigned odd0 = __ballot_sync(0xffffffffu, h.v[0][1].y != 0.f) >> ((SL - 1) * CL);
+        const unsigned odd1 = __ballot_sync(0xffffffffu, h.v[1][1].y != 0.f) >> ((SL - 1) * CL);
+        unsigned which = 0;                              // bits of the pairs' channels, side by side
+#pragma unroll
+        for (int c = 0; c < CL; ++c) which |= (odd0 >> c & 1) << (2 * c) | (odd1 >> c & 1) << (2 * c + 1);
+        which &= ~0u >> (32 - cols);
+        if (which)
+            sum_again<K, W, E, Td>(p, seq, g, d0, first, t0, t1, which,
+                                   [](int k, int c) { return k % SL * CL + c / 2; });
+    }
     // the warp that wrote the carried states last
     if (a.fin && last && warp == (rounds == 0 ? 0 : W - 1)) {
         for (int nb = 0; nb < NB; ++nb) {
@@ -875,7 +960,8 @@ cudaError_t launch_cut(ScanParams p, int64_t units, int ranks, cudaStream_t st) 
     const size_t shared = bytes(p.nblocks);
     constexpr size_t most = bytes(SL == 4 ? kMaxSelectiveStates / 16 : 1);     // two lanes: up to 8 states
     static_assert(most <= 227 * 1024, "");
-    auto kernel = cut_scan_kernel<E, Td, SL, kSegments>;
+    auto kernel = p.a.N % (4 * SL) != 0 || !p.a.Dskip ? cut_scan_kernel<E, Td, SL, kSegments, true>
+                                                      : cut_scan_kernel<E, Td, SL, kSegments, false>;
     const cudaError_t e = allow_shared(kernel, most);
     if (e != cudaSuccess) return e;
     p.ranked = p.a.cu && p.a.nseq <= kRanked && units > 148 && units <= 5 * 148;
@@ -1000,7 +1086,7 @@ __device__ __forceinline__ void store_piece(float* p, const float (&v)[1]) { __s
 // R rows a thread, Q = R / (lanes that prepare them): a lane prepares rows q (R / Q) + j, q < Q.
 // Addresses are walked: a row or token further costs an addition, where a product of 64-bit
 // strides costs several instructions and made up half of the kernel's.
-template <typename E, typename Td, int V, int KP, int R, int Q>
+template <typename E, typename Td, int V, int KP, int R, int Q, bool kCare>
 __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
     step_kernel(const __grid_constant__ StepParams p) {
     constexpr int PL = R / Q;                            // lanes that prepare rows, at most L
@@ -1105,9 +1191,12 @@ __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
                 F Bf[M], Cf[M];
                 Bv[r][k].widen(Bf);
                 Cv[r][k].widen(Cf);
+                // pieces past N, which only the second half can be, stay 0 beside infinite steps
+                const bool some = !kCare || k < KP / 2 || in[k];
+                const float dtk = some ? dtr : 0.f, duk = some ? du : 0.f;
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    h[r][k][m] = fma_(decay_of(A[k][m], all<F>(dtr)), h[r][k][m], mul_(Bf[m], all<F>(du)));
+                    h[r][k][m] = fma_(decay_of(A[k][m], all<F>(dtk)), h[r][k][m], mul_(Bf[m], all<F>(duk)));
                     sum = fma_(Cf[m], h[r][k][m], sum);
                 }
             }
@@ -1136,8 +1225,10 @@ __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
             for (int q = 0; q < Q; ++q) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], off);
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-            if (j < PL && q * PL + own < rows)
-                store_elem(y + q * PL * a.T * a.D, (a.Dskip ? fmaf(skip, u[q], sum[q]) : sum[q]) * gate[q]);
+            if (j < PL && q * PL + own < rows) {
+                const float with = fmaf(skip, u[q], sum[q]);
+                store_elem(y + q * PL * a.T * a.D, (!kCare || a.Dskip ? with : sum[q]) * gate[q]);
+            }
     }
     float* s = state;
 #pragma unroll
@@ -1152,10 +1243,12 @@ cudaError_t launch_rows(const StepParams& p, int64_t blocks, cudaStream_t st) {
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     // as many lanes prepare rows as there are, of the L lanes (32 with more than one piece)
     constexpr int kMost = R < 4 ? R : 4;
-    auto kernel = step_kernel<E, Td, V, KP, R, R / kMost>;
+    const bool care = (int64_t)KP * p.L * V != p.a.N || !p.a.Dskip;
+    auto kernel = care ? step_kernel<E, Td, V, KP, R, R / kMost, true> : step_kernel<E, Td, V, KP, R, R / kMost, false>;
     if constexpr (KP == 1 && R > 1) {
-        if (p.L == 1) kernel = step_kernel<E, Td, V, KP, R, R>;
-        if (p.L == 2) kernel = step_kernel<E, Td, V, KP, R, R / 2>;
+        if (p.L == 1) kernel = care ? step_kernel<E, Td, V, KP, R, R, true> : step_kernel<E, Td, V, KP, R, R, false>;
+        if (p.L == 2)
+            kernel = care ? step_kernel<E, Td, V, KP, R, R / 2, true> : step_kernel<E, Td, V, KP, R, R / 2, false>;
     }
     kernel<<<(unsigned)blocks, kStepThreads, 0, st>>>(p);
     return cudaGetLastError();

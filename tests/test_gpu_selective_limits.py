@@ -89,3 +89,31 @@ def test_scan_infinite_inputs(ssd, b, T, D, N, dtype):
 @pytest.mark.parametrize("b,D", [(2, 40), (18, 4800)])
 def test_step_infinite_inputs(ssd, b, D, N, dtype):
     infinite_step(ssd, b, D, N, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [1, 3, 5, 11, 20])
+@pytest.mark.parametrize("b,T,D", FORMS + [(1, 16, 40), (4, 140, 4800)])
+def test_scan_infinite_inputs_beside_padded_states(ssd, b, T, D, N, dtype):
+    """State counts that leave some of a kernel's states empty, which stay 0 whatever the input is."""
+    infinite_scan(ssd, b, T, D, N, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [3, 5, 12, 36, 70, 100, 130, 200])
+@pytest.mark.parametrize("b,D", [(2, 40), (18, 4800)])
+def test_step_infinite_inputs_beside_padded_states(ssd, b, D, N, dtype):
+    infinite_step(ssd, b, D, N, dtype)
+
+
+@pytest.mark.parametrize("N", [1, 5, 11, 16, 20])
+@pytest.mark.parametrize("b,T,D", FORMS)
+def test_scan_nan_inputs(ssd, b, T, D, N):
+    """NaN stays in its channel and behind its token, beside padded states too."""
+    d = positive(b, T, D, N, "bf16")
+    yc, fc = ssd.ssd_selective_scan(**d, return_final_states=True)
+    d["u"][0, T // 2, D - 3] = float("nan")
+    y, fin = ssd.ssd_selective_scan(**d, return_final_states=True)
+    assert torch.isnan(y[0, T // 2:, D - 3]).all() and torch.isnan(fin[0, D - 3]).all()
+    y[0, T // 2:, D - 3], fin[0, D - 3] = yc[0, T // 2:, D - 3], fc[0, D - 3]
+    assert torch.equal(y, yc) and torch.equal(fin, fc)
