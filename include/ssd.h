@@ -423,7 +423,7 @@ typedef struct {
  *   u, dt, z           [b, T, D], strides as given; z NULL: no gate.
  *   A                  [D, N] fp32 (not checked for sign; where the decays' product
  *                      over a stretch of tokens overflows fp32 the result can be
- *                      inf or NaN).
+ *                      inf or NaN). -inf keeps nothing past a step above 0.
  *   B, C               [b, T, G, N], strides as given ([G, N] contiguous).
  *   D, dt_bias         [D] fp32 or NULL (0).
  *   initial_states     [b, D, N] fp32 or NULL (zeros).

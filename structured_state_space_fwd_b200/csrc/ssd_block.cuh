@@ -60,6 +60,14 @@ __device__ __forceinline__ T all(float v) {
 constexpr float kCentre = 1.5e-8f;
 template <typename T>
 __device__ __forceinline__ T decay_of(T x, T y) { return ex2(fma_(x, y, all<T>(kCentre))); }
+// A decay's rate A in powers of 2, finite below (NaN stays NaN): A = -inf, or one whose product with log2(e)
+// is, forgets at every step above 0, and the steps of 0 behind a sequence's end leave the state as it is.
+__device__ __forceinline__ float rate_of(float a) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a * kLog2e), "f"(-3.402823466e38f));
+    return r;
+}
+__device__ __forceinline__ float2 rate_of(float2 a) { return make_float2(rate_of(a.x), rate_of(a.y)); }
 // -|v|, not below -126: exp is 0 there; keeps infinities finite, and NaN NaN
 __device__ __forceinline__ float neg_abs(float v) {
     const float m = -fabsf(v);

@@ -239,7 +239,7 @@ __device__ __noinline__ void sum_again(const ScanParams& p, int64_t seq, int64_t
 #pragma unroll 1
             for (int i = 0; i * 32 + lane < N; ++i) {
                 const int n = i * 32 + lane;
-                h[i] = fmaf(decay_of(dt, a.A[d * N + n] * kLog2e), h[i], dt * u * to_float(B[n]));
+                h[i] = fmaf(decay_of(dt, rate_of(a.A[d * N + n])), h[i], dt * u * to_float(B[n]));
                 sum = fmaf(to_float(C[n]), h[i], sum);
                 lost |= h[i] != h[i];
             }
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
             for (int x = 0; x < 2; ++x) {
                 const int n = nb * NS + j * (2 * P) + 2 * i + x;
                 v[x] = a.init && n < N ? a.init[(seq * a.D + d) * N + n] : 0.f;
-                r[x] = n < N ? a.A[d * N + n] * kLog2e : 0.f;
+                r[x] = n < N ? rate_of(a.A[d * N + n]) : 0.f;
             }
             A[i] = make_float2(r[0], r[1]);
             if (warp == 0) {
@@ -644,12 +644,13 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
     const float2 skip = a.Dskip ? make_float2(a.Dskip[da], a.Dskip[db]) : both(0.f);
     const float2 bias = a.dt_bias ? make_float2(a.dt_bias[da], a.dt_bias[db]) : both(0.f);
 
-    auto row_of = [&](const float* base, int64_t d, int nb, float scale, float2& lo, float2& hi) {
+    auto row_of = [&](const float* base, int64_t d, int nb, bool rates, float2& lo, float2& hi) {
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int n = nb * NS + j * 4 + i;
-            v[i] = base && n < N ? base[d * N + n] * scale : 0.f;
+            v[i] = base && n < N ? base[d * N + n] : 0.f;
+            if (rates) v[i] = rate_of(v[i]);
         }
         lo = make_float2(v[0], v[1]);
         hi = make_float2(v[2], v[3]);
@@ -658,8 +659,8 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
     if (warp == 0) {
         for (int nb = 0; nb < NB; ++nb) {
             States h;
-            row_of(init, da, nb, 1.f, h.v[0][0], h.v[0][1]);
-            row_of(init, db, nb, 1.f, h.v[1][0], h.v[1][1]);
+            row_of(init, da, nb, false, h.v[0][0], h.v[0][1]);
+            row_of(init, db, nb, false, h.v[1][0], h.v[1][1]);
             h.store(carry + nb * 64 + lane);
             if (kSegments) {
                 h.fill(0.f);
@@ -717,8 +718,8 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
     };
     States A;
     auto rates = [&](int nb) {
-        row_of(a.A, da, nb, kLog2e, A.v[0][0], A.v[0][1]);
-        row_of(a.A, db, nb, kLog2e, A.v[1][0], A.v[1][1]);
+        row_of(a.A, da, nb, true, A.v[0][0], A.v[0][1]);
+        row_of(a.A, db, nb, true, A.v[1][0], A.v[1][1]);
     };
     if (NB == 1) rates(0);
     // The segment's rounds; kOut: with outputs, from the states in `carry`, else only what it leaves
@@ -1139,7 +1140,7 @@ __global__ void __launch_bounds__(kStepThreads, V * KP * R <= 16 ? 6 : 1)
         if (in[k]) q.load(a.A + dc * N + (j + k * L) * V, p.a_wide);
         q.widen(A[k]);
 #pragma unroll
-        for (int m = 0; m < M; ++m) A[k][m] = mul_(A[k][m], all<F>(kLog2e));
+        for (int m = 0; m < M; ++m) A[k][m] = rate_of(A[k][m]);
     }
     const float skip = a.Dskip ? a.Dskip[dc] : 0.f, bias = a.dt_bias ? a.dt_bias[dc] : 0.f;
     E* y = static_cast<E*>(a.y) + (b0 + own) * a.T * a.D + dc;

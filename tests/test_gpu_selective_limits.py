@@ -117,3 +117,22 @@ def test_scan_nan_inputs(ssd, b, T, D, N):
     assert torch.isnan(y[0, T // 2:, D - 3]).all() and torch.isnan(fin[0, D - 3]).all()
     y[0, T // 2:, D - 3], fin[0, D - 3] = yc[0, T // 2:, D - 3], fc[0, D - 3]
     assert torch.equal(y, yc) and torch.equal(fin, fc)
+
+
+@pytest.mark.parametrize("rate", [float("-inf"), -3e38])
+@pytest.mark.parametrize("N", [1, 5, 16, 20])
+@pytest.mark.parametrize("b,T,D", FORMS + [(1, 18, 40), (1, 1, 40)])
+def test_scan_rates_without_bound(ssd, b, T, D, N, rate):
+    """A = -inf, or so large that its exponent overflows: nothing is kept from one token to the next,
+    also where the last tile is not full."""
+    for dtype in ("f32", "bf16"):
+        d = cuda(inputs(b, T, D, 1, N, dtype, seed=3))
+        d["dt"] = d["dt"].abs() * 4                              # steps of at least softplus(-7) = 9e-4
+        d["A"][1] = -1e6
+        y, fin = ssd.ssd_selective_scan(**d, return_final_states=True)
+        d["A"][1] = rate
+        y1, fin1 = ssd.ssd_selective_scan(**d, return_final_states=True)
+        assert torch.equal(y, y1) and torch.equal(fin, fin1)
+        state = d.pop("initial_states")
+        y2 = ssd.ssd_selective_step(**d, state=state)
+        assert torch.isfinite(y2).all() and torch.isfinite(state).all()
