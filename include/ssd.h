@@ -424,6 +424,8 @@ typedef struct {
  *   A                  [D, N] fp32 (not checked for sign; where the decays' product
  *                      over a stretch of tokens overflows fp32 the result can be
  *                      inf or NaN). -inf keeps nothing past a step above 0.
+ *                      An infinite state stays infinite while the decays of a
+ *                      token, and of 16, do not underflow; NaN otherwise.
  *   B, C               [b, T, G, N], strides as given ([G, N] contiguous).
  *   D, dt_bias         [D] fp32 or NULL (0).
  *   initial_states     [b, D, N] fp32 or NULL (zeros).

@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -909,8 +910,11 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            h.v[c][i] = fma_(ex2(mul_(both(c ? sum.y : sum.x), A.v[c][i])), h.v[c][i], l[c][i]);
+                        for (int i = 0; i < 2; ++i) {
+                            // not 0, however long the segment: an infinite state stays infinite
+                            const float2 e = ex2(mul_(both(c ? sum.y : sum.x), A.v[c][i]));
+                            h.v[c][i] = fma_(make_float2(fmaxf(e.x, FLT_MIN), fmaxf(e.y, FLT_MIN)), h.v[c][i], l[c][i]);
+                        }
                 }
                 h.store(carry + nb * 64 + lane);
             }

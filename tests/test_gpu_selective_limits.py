@@ -136,3 +136,13 @@ def test_scan_rates_without_bound(ssd, b, T, D, N, rate):
         state = d.pop("initial_states")
         y2 = ssd.ssd_selective_step(**d, state=state)
         assert torch.isfinite(y2).all() and torch.isfinite(state).all()
+
+
+@pytest.mark.parametrize("N", [1, 16, 20])
+@pytest.mark.parametrize("b,T,D", FORMS)
+def test_scan_infinite_states_stay(ssd, b, T, D, N):
+    """An infinite state stays infinite, also where the decays of a cluster's segment multiply to less
+    than fp32 holds."""
+    d = positive(b, T, D, N, "f32", rate=8.0)
+    d["u"][0, 5, 3] = float("inf")
+    run_infinite(ssd, d, False, 5, 3)
