@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
     }
     copy_wait<0>();
     if (kCare && N % NS != 0) {
+        __syncwarp();                                        // lanes part at the stores; the barrier takes whole warps
         asm volatile("bar.sync 2, 64;" ::: "memory");        // (0 and 1 are the warps' own)
         const bool odd = in && j == S - 1 && carry[(NB * P - 1) * 32].y != 0.f;
         const unsigned which = __ballot_sync(0xffffffffu, odd) >> ((S - 1) * CH);
@@ -952,7 +953,10 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
             }
         }
     }
-    if constexpr (kSegments) cluster_wait();             // others read this CTA's shared memory until here
+    if constexpr (kSegments) {
+        __syncwarp();                                    // lanes part at the stores above; the barrier is for whole warps
+        cluster_wait();                                  // others read this CTA's shared memory until here
+    }
 }
 
 template <typename E, typename Td, int SL, bool kSegments>
