@@ -528,10 +528,14 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     };
     const size_t shared = bytes(p.nblocks);
     // 6 CTAs an SM (168 registers), or 8 where that saves a wave (1024 tokens, 16 states, bf16: 960 units 132
-    // us with 8, 140 with 6; 800 units 105 and 101). Blocks of states gain from warps instead (9).
+    // us with 8, 140 with 6; 800 units 105 and 101).
+    // Blocks of states: in bf16 9 (96 registers; 128 states of 4 x 512 x 4096 575 us, 642 with 6; 64 states
+    // of 16 x 512 x 5120 1175 and 1186), but in fp32 6, whose shared memory leaves room for fewer (32 states
+    // of 16 x 256 x 4096 260 us, 302 with 9; 256 states of 8 x 128 x 5120 783 and 1176).
+    constexpr int kCtas = kBlocks && sizeof(E) == 2 ? 9 : 6;
     const bool care = a.N % NS != 0 || !a.Dskip;
-    auto kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, kBlocks ? 9 : 6>
-                       : wide_scan_kernel<E, Td, NS, S, kBlocks, false, kBlocks ? 9 : 6>;
+    auto kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, kCtas>
+                       : wide_scan_kernel<E, Td, NS, S, kBlocks, false, kCtas>;
     if constexpr (!kBlocks)
         if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
             kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, 8>
