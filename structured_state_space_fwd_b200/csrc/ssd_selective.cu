@@ -267,8 +267,8 @@ __device__ __noinline__ void sum_again(const ScanParams& p, int64_t seq, int64_t
 // turn and hand the states over through shared memory: while one runs the states through its tile,
 // the other computes the steps of its next and finishes its last. 168 registers, which keep the next
 // token's decays, B and C in flight, are worth more than twice the warps (4 x 2048 tokens of 5120
-// channels, 16 states, bf16: 320 us with 6 CTAs an SM, 345 with 8, 338 with 9, 336 with 11; one lane a
-// channel 353; four lanes for a pair of channels 349), except where states come in blocks.
+// channels, 16 states, bf16: 321 us with 6 CTAs an SM, 328 with 8, 327 with 9, 330 with 11; one lane a
+// channel 353; four lanes for a pair of channels 349; but see launch_wide).
 constexpr int kWideTok = 16, kWideWarps = 2;
 
 template <typename E, typename Td, int NS, int S>
@@ -527,8 +527,9 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
         return kWideWarps * sizeof(WideMem<E, Td, NS, S>) + nblocks * (NS / S) * 32 * 4 * (kBlocks ? 2 : 1);
     };
     const size_t shared = bytes(p.nblocks);
-    // 6 CTAs an SM (168 registers), or 8 where that saves a wave (1024 tokens, 16 states, bf16: 960 units 132
-    // us with 8, 140 with 6; 800 units 105 and 101).
+    // 6 CTAs an SM (168 registers), or 8 (128) where that makes fewer waves. 1024 tokens, 16 states, bf16, us
+    // with 6 and with 8: 800 units 101, 105; 960 140, 132; 1280 165, 169; 1920 229, 224; 2560 286, 285 (as
+    // many waves: 6); 3840 410, 403; 5120 557, 548; 10240 1070, 1049.
     // Blocks of states: in bf16 9 (96 registers; 128 states of 4 x 512 x 4096 575 us, 642 with 6; 64 states
     // of 16 x 512 x 5120 1175 and 1186), but in fp32 6, whose shared memory leaves room for fewer (32 states
     // of 16 x 256 x 4096 260 us, 302 with 9; 256 states of 8 x 128 x 5120 783 and 1176).
@@ -542,9 +543,10 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
                           : wide_scan_kernel<E, Td, NS, S, kBlocks, false, 8>;
     const cudaError_t e = allow_shared(kernel, bytes(kBlocks ? kMaxSelectiveStates / NS : 1));
     if (e != cudaSuccess) return e;
-    // Over one to five waves of 6 CTAs an SM the order decides the tail (8192 tokens of 2048 channels in 16
-    // documents 134 us ranked, 176 in the pack's order); with more, short documents are better spread
-    // between long ones (64 documents 166 ranked, 150 not).
+    // From one wave of 8 CTAs an SM to four the order decides the tail; with more, short documents are better
+    // spread between long ones. 8192 tokens, 16 states, bf16, us ranked and in the pack's order: 16 documents
+    // of 2048 channels (2048 units) 139, 176; 16 of 4096 (4096) 236, 270; 40 of 2048 (5120) 142, 152; 48 of
+    // 2048 (6144) 145, 146; 64 of 2048 (8192) 157, 149. Within a wave: 4 of 4096 (1024) 438, 341.
     p.ranked = a.cu && a.nseq <= kRanked && units > 8 * 148 && units <= 32 * 148;
     kernel<<<(unsigned)units, kWideWarps * 32, shared, st>>>(p);
     return cudaGetLastError();
@@ -977,6 +979,8 @@ cudaError_t launch_cut(ScanParams p, int64_t units, int ranks, cudaStream_t st) 
                                                       : cut_scan_kernel<E, Td, SL, kSegments, false>;
     const cudaError_t e = allow_shared(kernel, most);
     if (e != cudaSuccess) return e;
+    // as in launch_wide, over one to five waves of a CTA an SM (8192 tokens, bf16: 16 documents of 512
+    // channels, 48 states 149 us ranked, 169 not; 10 of 640, 32 states 151, 172); more make the uncut form
     p.ranked = p.a.cu && p.a.nseq <= kRanked && units > 148 && units <= 5 * 148;
     cudaLaunchAttribute cluster;
     cluster.id = cudaLaunchAttributeClusterDimension;
