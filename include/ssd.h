@@ -356,8 +356,9 @@ typedef struct {
  *   final_states       [b, W-1, C] dtype or NULL (not written): the last W - 1
  *                      tokens of (initial_states | u), so of both when T < W - 1.
  * fp32 arithmetic, y rounded once to dtype. Pointers are aligned to their
- * element; 16-byte aligned tensors, strides and splits are read and written 16
- * bytes at a time. No output may overlap u's span (first to last element), any
+ * element; 4 channels are read and written at a time (8 bytes of bf16, 16 of
+ * fp32) where the sizes of the split and u's strides are multiples of 4 and the
+ * tensors and states start on that many bytes. No output may overlap u's span (first to last element), any
  * other input or another output. One kernel launch, no workspace.
  */
 SSD_API ssd_status_t ssd_causal_conv1d(const ssd_conv_shape_t* shape, const void* u, const float* weight,

@@ -32,7 +32,8 @@ __device__ __forceinline__ float rcp(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// v / (1 + exp(-v)): 0 for very negative v (the divisor is inf), NaN for -inf as the formula.
+// v / (1 + exp(-v)): 0 below about -87.3, where the reciprocal of a divisor above 2^126 is flushed (exact:
+// above -1.1e-36), NaN for -inf as the formula.
 __device__ __forceinline__ float silu(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
 
 // Packed pairs of fp32 values, and the same names for one.
@@ -80,7 +81,7 @@ __device__ __forceinline__ float2 positive(float2 v) { return make_float2(positi
 // s = e / (2 + e) in (0, 1/3], log1p(e) = 2 atanh(s) = 2 s (1 + q P(q)), q = s^2 in (0, 1/9]; P
 // interpolates (atanh(sqrt q) / sqrt q - 1) / q in four Chebyshev nodes, which leaves a relative
 // error of 1.6e-8. So small steps keep their precision, which log(1 + e) would lose; the rounding
-// of the exponent v log2(e) moves e by at most 2^-24 |v|.
+// of the exponent v log2(e), of its product and of the constant, moves e by at most 1.22 2^-24 |v|.
 template <typename T>
 __device__ __forceinline__ T softplus(T v) {
     const T e = ex2(mul_(neg_abs(v), all<T>(kLog2e)));

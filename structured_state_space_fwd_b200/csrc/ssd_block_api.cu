@@ -32,11 +32,11 @@ ssd_status_t cuda_status(const char* what, cudaError_t e) {
     return SSD_ERR_CUDA;
 }
 
-// Bytes from the first to behind the last element of an input of b x T rows of n elements.
 bool stride_ok(const ssd_strides_t& s, int64_t b, int64_t T) {
     if (s.batch < 0 || s.row < 0) return false;
     return (double)s.batch * (double)b + (double)s.row * (double)T <= kMaxElems;
 }
+// Bytes from the first to behind the last element of an input of b x T rows of n elements.
 size_t span(const ssd_strides_t& s, int64_t b, int64_t T, int64_t n, size_t es) {
     if (b == 0 || T == 0) return 0;
     return (size_t)((b - 1) * s.batch + (T - 1) * s.row + n) * es;
@@ -78,8 +78,7 @@ ssd_status_t check_conv_shape(const ssd_conv_shape_t* s) {
     return SSD_OK;
 }
 
-// Shared by the three convolution entries; `init` and `fin` are [nseq, W-1, C], in_place when the
-// state is both.
+// Shared by the three convolution entries; `init` and `fin` are [nseq, W-1, C] (the step's state is `fin`).
 ssd_status_t check_conv(const ssd_conv_shape_t* s, int64_t nseq, const void* u, const float* weight,
                         const float* bias, const int32_t* cu, const void* init, void* const* y, void* fin,
                         ssd::ConvArgs* a) {
