@@ -208,8 +208,9 @@ __device__ __forceinline__ void quad_of(const __nv_bfloat16* p, float2* v) {
 // end of the sequence, and reaches y, which may be infinite instead. So where the last padded state is not
 // 0 at the end, each warp goes over the y that it stored: where that is NaN, the sum over the N states
 // alone takes its place. The kernels' loops have no part in this (checks of every tile's dt u, or of its
-// states, cost 3 to 20 %; this up to 10, 2 on average). Where there is no D, 0 times an infinite u may not be
-// added either. kCare, of the kernels: the call has padded states or no D; else there is nothing to look after.
+// states, cost 3 to 20 %; this up to 10, 2 on average. Going over a channel again costs 0.8 us a token and
+// channel of the warp.) Where there is no D, 0 times an infinite u may not be added either. kCare, of the
+// kernels: 2 with padded states, 1 without them or D, 0 else, with nothing to look after.
 //
 // Warp w has stored the tiles of kTok tokens w, w + kWarps, .. from token `from` on to `end`; the sequence
 // starts at t0. which: bits of the channels; owner(k, c): the lane that stored token k of a tile. A lane has
@@ -259,6 +260,8 @@ __device__ __noinline__ void sum_again(const ScanParams& p, int64_t seq, int64_t
     }
 }
 
+inline int care_of(const SelectiveArgs& a, int states) { return a.N % states != 0 ? 2 : a.Dskip ? 0 : 1; }
+
 // ---- many channels -----------------------------------------------------------
 //
 // S = 2 lanes (1 with up to 4 states) hold a channel's states, 8 each of 16 at a time, and every
@@ -302,7 +305,7 @@ __device__ __forceinline__ float2 tokens_of(const E (*rows)[CH], int k, int ch) 
 // S: lanes of a channel, each with NS / S of the states and every S-th pair of tokens to prepare and
 // finish. kBlocks: more states than NS, which the inner loops then take a block at a time. kCtas: CTAs an
 // SM that the registers are capped for.
-template <typename E, typename Td, int NS, int S, bool kBlocks, bool kCare, int kCtas>
+template <typename E, typename Td, int NS, int S, bool kBlocks, int kCare, int kCtas>
 __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kWideTok, P = NS / S / 2, W = kWideWarps, CH = 32 / S, Q = K / 2 / S;
     using Mem = WideMem<E, Td, NS, S>;
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const float2 with = fma_(skip, tokens_of(m.u[sr], 2 * (q * S + j), ch), yv[q]);
-            yv[q] = !kCare || a.Dskip ? with : yv[q];
+            yv[q] = kCare == 0 || (kCare == 2 && a.Dskip) ? with : yv[q];
         }
         if (zb) {
 #pragma unroll
@@ -495,7 +498,7 @@ __global__ void __launch_bounds__(kWideWarps * 32, kCtas) wide_scan_kernel(const
         }
     }
     copy_wait<0>();
-    if (kCare && N % NS != 0) {
+    if constexpr (kCare == 2) {
         __syncwarp();                                        // lanes part at the stores; the barrier takes whole warps
         asm volatile("bar.sync 2, 64;" ::: "memory");        // (0 and 1 are the warps' own)
         const bool odd = in && j == S - 1 && carry[(NB * P - 1) * 32].y != 0.f;
@@ -534,13 +537,15 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     // of 16 x 512 x 5120 1175 and 1186), but in fp32 6, whose shared memory leaves room for fewer (32 states
     // of 16 x 256 x 4096 260 us, 302 with 9; 256 states of 8 x 128 x 5120 783 and 1176).
     constexpr int kCtas = kBlocks && sizeof(E) == 2 ? 9 : 6;
-    const bool care = a.N % NS != 0 || !a.Dskip;
-    auto kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, kCtas>
-                       : wide_scan_kernel<E, Td, NS, S, kBlocks, false, kCtas>;
+    const int care = care_of(a, NS);
+    auto kernel = care == 2   ? wide_scan_kernel<E, Td, NS, S, kBlocks, 2, kCtas>
+                  : care == 1 ? wide_scan_kernel<E, Td, NS, S, kBlocks, 1, kCtas>
+                              : wide_scan_kernel<E, Td, NS, S, kBlocks, 0, kCtas>;
     if constexpr (!kBlocks)
         if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
-            kernel = care ? wide_scan_kernel<E, Td, NS, S, kBlocks, true, 8>
-                          : wide_scan_kernel<E, Td, NS, S, kBlocks, false, 8>;
+            kernel = care == 2   ? wide_scan_kernel<E, Td, NS, S, kBlocks, 2, 8>
+                     : care == 1 ? wide_scan_kernel<E, Td, NS, S, kBlocks, 1, 8>
+                                 : wide_scan_kernel<E, Td, NS, S, kBlocks, 0, 8>;
     const cudaError_t e = allow_shared(kernel, bytes(kBlocks ? kMaxSelectiveStates / NS : 1));
     if (e != cudaSuccess) return e;
     // From one wave of 8 CTAs an SM to four the order decides the tail; with more, short documents are better
@@ -605,7 +610,7 @@ struct States {
     }
 };
 
-template <typename E, typename Td, int SL, bool kSegments, bool kCare>
+template <typename E, typename Td, int SL, bool kSegments, int kCare>
 __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __grid_constant__ ScanParams p) {
     constexpr int K = kCutTok, W = kCutWarps;
     constexpr int CL = 32 / SL, CH = 2 * CL, NS = 4 * SL;
@@ -878,7 +883,7 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
 #pragma unroll
             for (int q = 0; q < K / SL; ++q) {
                 const float2 with = fma_(skip, pair_of(&m.u[sr][q * SL + j][2 * cp]), ysum[q]);
-                ysum[q] = !kCare || a.Dskip ? with : ysum[q];
+                ysum[q] = kCare == 0 || (kCare == 2 && a.Dskip) ? with : ysum[q];
             }
             if (zb) {
 #pragma unroll
@@ -929,7 +934,7 @@ __global__ void __launch_bounds__(kCutWarps * 32, 1) cut_scan_kernel(const __gri
         cluster_arrive();
     }
     run(std::true_type{}, carry);
-    if (kCare && N % NS != 0) {
+    if constexpr (kCare == 2) {
         __syncthreads();
         States h;
         h.load(carry + (NB - 1) * 64 + lane);
@@ -975,8 +980,10 @@ cudaError_t launch_cut(ScanParams p, int64_t units, int ranks, cudaStream_t st) 
     const size_t shared = bytes(p.nblocks);
     constexpr size_t most = bytes(SL == 4 ? kMaxSelectiveStates / 16 : 1);     // two lanes: up to 8 states
     static_assert(most <= 227 * 1024, "");
-    auto kernel = p.a.N % (4 * SL) != 0 || !p.a.Dskip ? cut_scan_kernel<E, Td, SL, kSegments, true>
-                                                      : cut_scan_kernel<E, Td, SL, kSegments, false>;
+    const int care = care_of(p.a, 4 * SL);
+    auto kernel = care == 2   ? cut_scan_kernel<E, Td, SL, kSegments, 2>
+                  : care == 1 ? cut_scan_kernel<E, Td, SL, kSegments, 1>
+                              : cut_scan_kernel<E, Td, SL, kSegments, 0>;
     const cudaError_t e = allow_shared(kernel, most);
     if (e != cudaSuccess) return e;
     // as in launch_wide, over one to five waves of a CTA an SM (8192 tokens, bf16: 16 documents of 512
