@@ -535,12 +535,16 @@ cudaError_t launch_wide(ScanParams p, cudaStream_t st) {
     // many waves: 6); 3840 410, 403; 5120 557, 548; 10240 1070, 1049.
     // Blocks of states: in bf16 9 (96 registers; 128 states of 4 x 512 x 4096 575 us, 642 with 6; 64 states
     // of 16 x 512 x 5120 1175 and 1186), but in fp32 6, whose shared memory leaves room for fewer (32 states
-    // of 16 x 256 x 4096 260 us, 302 with 9; 256 states of 8 x 128 x 5120 783 and 1176).
+    // of 16 x 256 x 4096 260 us, 302 with 9; 256 states of 8 x 128 x 5120 783 and 1176). With padded states 6
+    // in bf16 too (20 states of 8 x 1024 x 5120 623 us, 695 with 9; 200 of 4 x 256 x 5120 586 and 759), unless B
+    // and C are copied element by element, which gains from warps (17 states of 8 x 512 x 5120 416 and 394).
     constexpr int kCtas = kBlocks && sizeof(E) == 2 ? 9 : 6;
     const int care = care_of(a, NS);
     auto kernel = care == 2   ? wide_scan_kernel<E, Td, NS, S, kBlocks, 2, kCtas>
                   : care == 1 ? wide_scan_kernel<E, Td, NS, S, kBlocks, 1, kCtas>
                               : wide_scan_kernel<E, Td, NS, S, kBlocks, 0, kCtas>;
+    if constexpr (kCtas == 9)
+        if (care == 2 && p.bc_bytes >= 4) kernel = wide_scan_kernel<E, Td, NS, S, kBlocks, 2, 6>;
     if constexpr (!kBlocks)
         if ((units + 8 * 148 - 1) / (8 * 148) < (units + 6 * 148 - 1) / (6 * 148))
             kernel = care == 2   ? wide_scan_kernel<E, Td, NS, S, kBlocks, 2, 8>
